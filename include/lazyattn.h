@@ -31,7 +31,8 @@
  *     never trap or hang.
  *   - Not thread-safe per pool: serialise calls that share a pool handle.
  *   - Entry points that launch work (store_doc, prefill, decode, materialize,
- *     resolve, decode_noalloc) need the pool's device to be the current one and
+ *     resolve, decode_noalloc, prefill_window, decode_window, prefill_mass,
+ *     decode_mass, evict) need the pool's device to be the current one and
  *     return LAZYATTN_EINVAL, launching nothing, when it is not.
  *
  * Input range (bf16 pools)
@@ -227,6 +228,8 @@ typedef struct lazyattn_batch {
 
 #define LAZYATTN_OP_PREFILL 0
 #define LAZYATTN_OP_DECODE 1
+#define LAZYATTN_OP_PREFILL_MASS 2
+#define LAZYATTN_OP_DECODE_MASS 3
 
 /* Human-readable name of a status code. Never NULL. */
 const char* lazyattn_status_string(int status);
@@ -286,8 +289,10 @@ int lazyattn_free_pages(lazyattn_pool_t pool, const int32_t* pages, int32_t n);
 int lazyattn_store_doc(lazyattn_pool_t pool, const void* k, const void* v, int32_t n_tokens,
                        void* stream, int32_t* out_pages, int32_t out_cap, int32_t* out_npages);
 
-/* Bytes of workspace that lazyattn_prefill (op = LAZYATTN_OP_PREFILL) or
- * lazyattn_decode (op = LAZYATTN_OP_DECODE) needs for this batch shape. The
+/* Bytes of workspace that lazyattn_prefill (op = LAZYATTN_OP_PREFILL),
+ * lazyattn_decode (LAZYATTN_OP_DECODE), lazyattn_prefill_mass
+ * (LAZYATTN_OP_PREFILL_MASS) or lazyattn_decode_mass (LAZYATTN_OP_DECODE_MASS)
+ * needs for this batch shape (the windowed calls: lazyattn_window_workspace_size). The
  * workspace is caller-allocated device memory, 256-byte aligned, and must be
  * ZERO-FILLED before its first use; every completed call leaves the parts that
  * must start at zero back at zero. Calls sharing one workspace must not
@@ -443,6 +448,100 @@ int lazyattn_get_device_status(lazyattn_pool_t pool, int32_t* out_status, int32_
 #define LAZYATTN_NOALLOC_SCRATCH_BYTES (16u << 20)
 int lazyattn_decode_noalloc(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q,
                             const void* k_new, const void* v_new, void* out, void* stream);
+
+/* ------------------------------------------------- keeping a long cache small
+ * Three operators that bound what a request reads or holds (no counterpart in
+ * the paper): windowed attention, the attention weight each cached token has
+ * received, and eviction by that weight. Document pages stay shared and
+ * unchanged throughout.
+ *
+ * Windowed attention: the key at logical position n is visible to the query at
+ * position m iff
+ *     n <= m  and  (m - n < window  or  n < sinks)
+ * i.e. the query's own token and the window - 1 positions before it, and the
+ * sequence's first `sinks` positions for good. window >= 1, sinks >= 0 (EINVAL).
+ * Positions are the entries' logical ones; entries may come in any order, and
+ * entries none of whose tokens is visible are not read. Rows that see no key get
+ * zeros. Everything else is as in lazyattn_prefill / lazyattn_decode: dtypes, key
+ * layouts, position encodings, flags, argument checks and the input range.
+ *
+ * lazyattn_window_workspace_size: bytes of workspace for lazyattn_prefill_window
+ * (op = LAZYATTN_OP_PREFILL) or lazyattn_decode_window (LAZYATTN_OP_DECODE) with
+ * this batch shape, window and sinks, under the rules of lazyattn_workspace_size.
+ * 0 on invalid arguments. */
+size_t lazyattn_window_workspace_size(lazyattn_pool_t pool, int32_t op, const lazyattn_batch* batch,
+                                      int32_t window, int32_t sinks);
+
+/* lazyattn_prefill under a window. workspace is optional, as there. */
+int lazyattn_prefill_window(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, void* out,
+                            int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes, void* stream);
+
+/* lazyattn_decode under a window: the token is appended, then attends under the
+ * rule above (unlike lazyattn_decode, tokens at positions past its own are not
+ * visible). A decode plan in the batch is ignored. workspace: at least
+ * lazyattn_window_workspace_size bytes (else EWORKSPACE). */
+int lazyattn_decode_window(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const void* k_new,
+                           const void* v_new, void* out, int32_t window, int32_t sinks, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Attention mass: the softmax weight each cached token receives, summed over query
+ * rows and over the query heads that share a KV head:
+ *     mass_out[i][h][s] = decay * mass_in[i][h][s] + sum over rows, heads of group h of p(row, token)
+ * for slot s of the batch's entry i and KV head h. mass_in and mass_out are float32
+ * device buffers [entries][n_kv_heads][16], parallel to batch->entries and 16-byte
+ * aligned; mass_in may be mass_out itself (other overlaps are not allowed) or NULL
+ * (nothing accumulated yet: decay is then unused). 0 <= decay <= 1: 1 accumulates, less fades
+ * older weight (EINVAL outside, or NaN). Every slot of the requests' entries is
+ * written: slots without a token get 0; what lies behind the last entry is left as
+ * it was. Scores and sums are held to fp32 accuracy for bf16 pools too (rotated q
+ * and k enter the products as the sum of two fp16 numbers), the order of every
+ * sum is fixed: equal calls give equal bits.
+ *
+ * lazyattn_prefill_mass: the rows of q (as in lazyattn_prefill: [total_q][n_q_heads][head_dim],
+ * q_offsets, q_start, keys visible up to a row's own position) observe the cache;
+ * no output is computed. Typically the last rows of a prompt, before the cache is cut down.
+ * Rows that see no key, and requests without rows, add nothing. Workspace:
+ * lazyattn_workspace_size(LAZYATTN_OP_PREFILL_MASS), required, no zero-fill needed. */
+int lazyattn_prefill_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const float* mass_in,
+                          float* mass_out, float decay, void* workspace, size_t workspace_bytes, void* stream);
+
+/* lazyattn_decode and, in the same pass over the keys, the mass of the step's one
+ * row: mass_out as above for the table after the append (the appended token's slot
+ * had no token before: give it 0 in mass_in, which holds for buffers that were
+ * zero-filled or written by these calls). A decode plan in the batch is ignored. A request with no free
+ * slot gets a zero output and keeps its mass (copied from mass_in, or 0). Workspace:
+ * lazyattn_workspace_size(LAZYATTN_OP_DECODE_MASS), as for lazyattn_decode. */
+int lazyattn_decode_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const void* k_new,
+                         const void* v_new, void* out, const float* mass_in, float* mass_out, float decay,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Eviction by accumulated weight: every KV head of every request keeps at most
+ * `budget` tokens of its own choice, copied, in table order, into pages of the
+ * request's own, at logical positions 0, 1, ... - keys carry no position, so
+ * nothing is re-encoded. With n tokens in the request's entries, all are kept if
+ * n <= budget; else the first `sinks`, the last `recent` and, of the others, those
+ * with the largest mass (equal ones: the earlier; NaN counts as the least), budget
+ * in all. budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget (EINVAL).
+ *   mass         float32 [entries][n_kv_heads][16], parallel to batch->entries
+ *   dst_entries  device uint64, in and out: request r's new entries are
+ *                [dst_offsets[r], dst_offsets[r+1]). The caller gives each a page
+ *                (distinct, and none that the batch's entries name) and the writable
+ *                bit; the call sets the starts to 0, 16, 32, ... and the counts of
+ *                tokens. Entries past the kept tokens come out empty: room for
+ *                lazyattn_decode to append into.
+ *   dst_offsets  int32 [R+1]; each request needs at least ceil(min(n, budget) / 16)
+ *   kept         int32 [R][n_kv_heads][budget]: the source logical position of each
+ *                kept token in order, -1 past the last
+ *   dst_mass     float32 [dst entries][n_kv_heads][16] parallel to dst_entries, or
+ *                NULL: the kept tokens' mass, 0 in empty slots
+ * The entries of a request that hold tokens must go up in position. A request where
+ * they do not, or whose entries or new pages are out of range or too few, keeps
+ * nothing (counts 0, kept -1, dst_mass 0) and LAZYATTN_ERANGE is recorded in the status word. The source pages are only read:
+ * free those of the request's own afterwards. Position-free pools only, without
+ * LAZYATTN_KEYS_PREROTATED (EINVAL): other layouts hold keys turned to their place. */
+int lazyattn_evict(lazyattn_pool_t pool, const lazyattn_batch* batch, const float* mass, int32_t budget, int32_t sinks,
+                   int32_t recent, uint64_t* dst_entries, const int32_t* dst_offsets, int32_t* kept, float* dst_mass,
+                   void* stream);
 
 #ifdef __cplusplus
 }

@@ -245,4 +245,20 @@ size_t prefill_ws_bytes(const lazyattn_pool& p, const lazyattn_batch& b, int spl
 int launch_prefill_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
                         __nv_bfloat16* out, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+// Windowed attention on CUDA cores (decode_qpos NULL: the batch's query rows).
+int launch_window_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void* q, void* out,
+                       const int32_t* decode_qpos, int32_t window, int32_t sinks, cudaStream_t stream);
+
+// Attention mass on CUDA cores, and the rows' outputs unless out is NULL; ws holds
+// mass_simt_ws_bytes for the number of query rows.
+size_t mass_simt_ws_bytes(const lazyattn_pool& p, int64_t rows);
+int launch_mass_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void* q, void* out,
+                     const int32_t* decode_qpos, const float* mass_in, float* mass_out, float decay, void* ws,
+                     cudaStream_t stream);
+
+// Eviction: selection and copy.
+int launch_evict(const lazyattn_pool& p, const lazyattn_batch& b, const float* mass, int32_t budget, int32_t sinks,
+                 int32_t recent, uint64_t* dst_entries, const int32_t* dst_offsets, int32_t* kept, float* dst_mass,
+                 cudaStream_t stream);
+
 }  // namespace lazyattn

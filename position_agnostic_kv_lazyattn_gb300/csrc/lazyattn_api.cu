@@ -315,6 +315,8 @@ int lazyattn_store_doc(lazyattn_pool_t pool, const void* k, const void* v, int32
     return LAZYATTN_OK;
 }
 
+static bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
 // A decode plan fits a batch when it was built for its number of requests and
 // the pool's head layout and key storage, and has been uploaded.
 static bool plan_fits(const lazyattn_pool* pool, const lazyattn_batch* b) {
@@ -333,12 +335,25 @@ static int check_batch(const lazyattn_pool* pool, const lazyattn_batch* b, int o
         ((b->flags & LAZYATTN_KEYS_PREROTATED) || (b->max_entries > 0 && !b->entry_delta)))
         return LAZYATTN_EINVAL;
     if (pool->d.position_encoding == LAZYATTN_POS_ALIBI && (b->flags & LAZYATTN_KEYS_PREROTATED)) return LAZYATTN_EINVAL;
-    if (op == LAZYATTN_OP_PREFILL) {
+    if (op == LAZYATTN_OP_PREFILL || op == LAZYATTN_OP_PREFILL_MASS) {
         if (b->total_q < 0 || b->max_q_len < 0 || !b->q_offsets || !b->q_start) return LAZYATTN_EINVAL;
     }
     if (op == LAZYATTN_OP_DECODE && b->decode_plan && pool->d.dtype == LAZYATTN_BF16 && !plan_fits(pool, b))
         return LAZYATTN_EINVAL;
     return LAZYATTN_OK;
+}
+
+// Check of a batch for the calls that ignore a decode plan.
+static int check_no_plan(const lazyattn_pool* pool, const lazyattn_batch* b, int op) {
+    if (!b) return LAZYATTN_EINVAL;
+    lazyattn_batch plain = *b;
+    plain.decode_plan = nullptr;
+    return check_batch(pool, &plain, op);
+}
+
+// Positions of the appended tokens, at the start of a decode workspace.
+static size_t qpos_bytes(const lazyattn_batch* b) {
+    return ((size_t)b->num_requests * sizeof(int32_t) + 255) & ~size_t(255);
 }
 
 size_t lazyattn_workspace_size(lazyattn_pool_t pool, int32_t op, const lazyattn_batch* batch) {
@@ -347,6 +362,8 @@ size_t lazyattn_workspace_size(lazyattn_pool_t pool, int32_t op, const lazyattn_
         const int splits = pool->d.dtype == LAZYATTN_BF16 ? prefill_splits(*pool, *batch) : 1;
         return splits > 1 ? prefill_ws_bytes(*pool, *batch, splits) : 256;
     }
+    if (op == LAZYATTN_OP_PREFILL_MASS) return mass_simt_ws_bytes(*pool, batch->total_q) + 256;
+    if (op == LAZYATTN_OP_DECODE_MASS) return qpos_bytes(batch) + mass_simt_ws_bytes(*pool, batch->num_requests);
     if (op != LAZYATTN_OP_DECODE) return 0;
     if (pool->d.dtype == LAZYATTN_F32) return (size_t)batch->num_requests * sizeof(int32_t) + 256;
     if (batch->decode_plan) return decode_plan_ws_bytes(*pool, *batch->decode_plan);
@@ -400,6 +417,104 @@ int lazyattn_decode(lazyattn_pool_t pool, const lazyattn_batch* batch, const voi
     if (rc != LAZYATTN_OK) return rc;
     return launch_decode_bf16(*pool, *batch, static_cast<const __nv_bfloat16*>(q),
                               static_cast<__nv_bfloat16*>(out), workspace, L, st);
+}
+
+static bool window_ok(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
+
+size_t lazyattn_window_workspace_size(lazyattn_pool_t pool, int32_t op, const lazyattn_batch* batch, int32_t window,
+                                      int32_t sinks) {
+    if ((op != LAZYATTN_OP_PREFILL && op != LAZYATTN_OP_DECODE) || check_no_plan(pool, batch, op) != LAZYATTN_OK ||
+        !window_ok(window, sinks))
+        return 0;
+    if (op == LAZYATTN_OP_PREFILL)
+        return window >= pool->d.max_position ? lazyattn_workspace_size(pool, op, batch) : 256;
+    return qpos_bytes(batch);
+}
+
+int lazyattn_prefill_window(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, void* out, int32_t window,
+                            int32_t sinks, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_batch(pool, batch, LAZYATTN_OP_PREFILL);
+    if (rc != LAZYATTN_OK) return rc;
+    if (!window_ok(window, sinks)) return LAZYATTN_EINVAL;
+    if (batch->total_q == 0) return LAZYATTN_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out)) return LAZYATTN_EINVAL;
+    rc = check_device(pool);
+    if (rc != LAZYATTN_OK) return rc;
+    // A window of every position hides nothing: the same call as without one.
+    if (window >= pool->d.max_position) return lazyattn_prefill(pool, batch, q, out, workspace, workspace_bytes, stream);
+    return launch_window_simt(*pool, *batch, q, out, nullptr, window, sinks, static_cast<cudaStream_t>(stream));
+}
+
+int lazyattn_decode_window(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const void* k_new,
+                           const void* v_new, void* out, int32_t window, int32_t sinks, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    int rc = check_no_plan(pool, batch, LAZYATTN_OP_DECODE);
+    if (rc != LAZYATTN_OK) return rc;
+    if (!window_ok(window, sinks) || !q || !k_new || !v_new || !out || !workspace) return LAZYATTN_EINVAL;
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) || !aligned256(workspace))
+        return LAZYATTN_EINVAL;
+    if (workspace_bytes < lazyattn_window_workspace_size(pool, LAZYATTN_OP_DECODE, batch, window, sinks))
+        return LAZYATTN_EWORKSPACE;
+    rc = check_device(pool);
+    if (rc != LAZYATTN_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int32_t* qpos = static_cast<int32_t*>(workspace);
+    rc = launch_decode_append(*pool, *batch, k_new, v_new, qpos, st);
+    if (rc != LAZYATTN_OK) return rc;
+    return launch_window_simt(*pool, *batch, q, out, qpos, window, sinks, st);
+}
+
+static bool mass_ok(const float* mass_in, const float* mass_out, float decay) {
+    return mass_out && aligned16(mass_in) && aligned16(mass_out) && decay >= 0.f && decay <= 1.f;   // NaN fails
+}
+
+int lazyattn_prefill_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const float* mass_in,
+                          float* mass_out, float decay, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_batch(pool, batch, LAZYATTN_OP_PREFILL_MASS);
+    if (rc != LAZYATTN_OK) return rc;
+    if (!mass_ok(mass_in, mass_out, decay) || !workspace || !aligned256(workspace)) return LAZYATTN_EINVAL;
+    if (batch->total_q > 0 && (!q || !aligned16(q))) return LAZYATTN_EINVAL;
+    if (workspace_bytes < lazyattn_workspace_size(pool, LAZYATTN_OP_PREFILL_MASS, batch)) return LAZYATTN_EWORKSPACE;
+    rc = check_device(pool);
+    if (rc != LAZYATTN_OK) return rc;
+    return launch_mass_simt(*pool, *batch, q, nullptr, nullptr, mass_in, mass_out, decay, workspace,
+                            static_cast<cudaStream_t>(stream));
+}
+
+int lazyattn_decode_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const void* k_new,
+                         const void* v_new, void* out, const float* mass_in, float* mass_out, float decay,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_no_plan(pool, batch, LAZYATTN_OP_DECODE_MASS);
+    if (rc != LAZYATTN_OK) return rc;
+    if (!q || !k_new || !v_new || !out || !workspace || !mass_ok(mass_in, mass_out, decay)) return LAZYATTN_EINVAL;
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) || !aligned256(workspace))
+        return LAZYATTN_EINVAL;
+    if (workspace_bytes < lazyattn_workspace_size(pool, LAZYATTN_OP_DECODE_MASS, batch)) return LAZYATTN_EWORKSPACE;
+    rc = check_device(pool);
+    if (rc != LAZYATTN_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int32_t* qpos = static_cast<int32_t*>(workspace);
+    rc = launch_decode_append(*pool, *batch, k_new, v_new, qpos, st);
+    if (rc != LAZYATTN_OK) return rc;
+    return launch_mass_simt(*pool, *batch, q, out, qpos, mass_in, mass_out, decay,
+                            static_cast<char*>(workspace) + qpos_bytes(batch), st);
+}
+
+int lazyattn_evict(lazyattn_pool_t pool, const lazyattn_batch* batch, const float* mass, int32_t budget, int32_t sinks,
+                   int32_t recent, uint64_t* dst_entries, const int32_t* dst_offsets, int32_t* kept, float* dst_mass,
+                   void* stream) {
+    int rc = check_no_plan(pool, batch, LAZYATTN_OP_DECODE);
+    if (rc != LAZYATTN_OK) return rc;
+    if ((batch->flags & LAZYATTN_KEYS_PREROTATED) || pool->d.key_storage != LAZYATTN_KEYS_POSITION_FREE)
+        return LAZYATTN_EINVAL;
+    if (budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget) return LAZYATTN_EINVAL;
+    if (!mass || !dst_entries || !dst_offsets || !kept || !aligned16(mass) || !aligned16(dst_mass) ||
+        (reinterpret_cast<uintptr_t>(dst_entries) & 7u))
+        return LAZYATTN_EINVAL;
+    rc = check_device(pool);
+    if (rc != LAZYATTN_OK) return rc;
+    return launch_evict(*pool, *batch, mass, budget, sinks, recent, dst_entries, dst_offsets, kept, dst_mass,
+                        static_cast<cudaStream_t>(stream));
 }
 
 int lazyattn_materialize(lazyattn_pool_t pool, const lazyattn_batch* batch, const uint64_t* dst_entries,

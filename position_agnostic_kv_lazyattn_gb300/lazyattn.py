@@ -22,6 +22,8 @@ LAZYATTN_BF16 = 1
 LAZYATTN_KEYS_PREROTATED = 1
 LAZYATTN_OP_PREFILL = 0
 LAZYATTN_OP_DECODE = 1
+LAZYATTN_OP_PREFILL_MASS = 2
+LAZYATTN_OP_DECODE_MASS = 3
 LAZYATTN_ROPE_DEFAULT = 0
 LAZYATTN_ROPE_LINEAR = 1
 LAZYATTN_ROPE_NTK = 2
@@ -101,6 +103,15 @@ def _load():
         "lazyattn_resolve": (ctypes.c_int, [vp, ctypes.POINTER(lazyattn_batch), vp, vp, i32, vp]),
         "lazyattn_get_device_status": (ctypes.c_int, [vp, P_i32, i32, vp]),
         "lazyattn_decode_noalloc": (ctypes.c_int, [vp, ctypes.POINTER(lazyattn_batch), vp, vp, vp, vp, vp]),
+        "lazyattn_window_workspace_size": (sz, [vp, i32, ctypes.POINTER(lazyattn_batch), i32, i32]),
+        "lazyattn_prefill_window": (ctypes.c_int, [vp, ctypes.POINTER(lazyattn_batch), vp, vp, i32, i32, vp, sz, vp]),
+        "lazyattn_decode_window": (ctypes.c_int, [vp, ctypes.POINTER(lazyattn_batch), vp, vp, vp, vp, i32, i32, vp, sz,
+                                                  vp]),
+        "lazyattn_prefill_mass": (ctypes.c_int, [vp, ctypes.POINTER(lazyattn_batch), vp, vp, vp, ctypes.c_float, vp, sz,
+                                                 vp]),
+        "lazyattn_decode_mass": (ctypes.c_int, [vp, ctypes.POINTER(lazyattn_batch), vp, vp, vp, vp, vp, vp,
+                                                ctypes.c_float, vp, sz, vp]),
+        "lazyattn_evict": (ctypes.c_int, [vp, ctypes.POINTER(lazyattn_batch), vp, i32, i32, i32, vp, vp, vp, vp, vp]),
         "lazyattn_check_batch_host": (ctypes.c_int, [vp, vp, i32, i32, i32, P_i32]),
         "lazyattn_decode_plan_create": (ctypes.c_int, [vp, vp, vp, vp, i32, ctypes.POINTER(vp)]),
         "lazyattn_decode_plan_device_bytes": (sz, [vp]),
@@ -123,6 +134,8 @@ EXPORTS = [
     "lazyattn_materialize", "lazyattn_resolve", "lazyattn_get_device_status", "lazyattn_decode_noalloc",
     "lazyattn_check_batch_host", "lazyattn_decode_plan_create", "lazyattn_decode_plan_device_bytes",
     "lazyattn_decode_plan_upload", "lazyattn_decode_plan_get_stats", "lazyattn_decode_plan_destroy",
+    "lazyattn_window_workspace_size", "lazyattn_prefill_window", "lazyattn_decode_window",
+    "lazyattn_prefill_mass", "lazyattn_decode_mass", "lazyattn_evict",
 ]
 NOALLOC_SCRATCH_BYTES = 16 << 20
 LAZYATTN_NOALLOC_SCRATCH_BYTES = NOALLOC_SCRATCH_BYTES
@@ -144,6 +157,16 @@ def _stream(stream) -> Optional[int]:
         import torch
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _dense(where: str, *tensors, dtype=None):
+    """Refuse tensors whose elements are not laid out densely (the C ABI takes plain
+    pointers) or, where dtype names are given, are of another type."""
+    for t in tensors:
+        if hasattr(t, "is_contiguous") and (not t.is_contiguous() or
+                                            (dtype and str(t.dtype).split(".")[-1] not in dtype)):
+            raise LazyAttnError(LAZYATTN_EINVAL, f"{where}: needs a contiguous tensor" +
+                                (f" of {' or '.join(dtype)}" if dtype else ""))
 
 
 # --------------------------------------------------------------------- host helpers
@@ -277,6 +300,58 @@ def lazyattn_decode_noalloc(pool: int, batch: lazyattn_batch, q, k_new, v_new, o
     device memory: uses the library's built-in scratch array instead."""
     _check(lib.lazyattn_decode_noalloc(pool, ctypes.byref(batch), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out),
                                        _stream(stream)), "lazyattn_decode_noalloc")
+
+
+def lazyattn_window_workspace_size(pool: int, op: int, batch: lazyattn_batch, window: int, sinks: int = 0) -> int:
+    return int(lib.lazyattn_window_workspace_size(pool, op, ctypes.byref(batch), window, sinks))
+
+
+def lazyattn_prefill_window(pool: int, batch: lazyattn_batch, q, out, window: int, sinks: int = 0, workspace=None,
+                            workspace_bytes: int = 0, stream=None):
+    """lazyattn_prefill where a key at position n is visible to a row at m iff
+    n <= m and (m - n < window or n < sinks)."""
+    _dense("lazyattn_prefill_window", q, out)
+    _check(lib.lazyattn_prefill_window(pool, ctypes.byref(batch), _ptr(q), _ptr(out), window, sinks, _ptr(workspace),
+                                       workspace_bytes, _stream(stream)), "lazyattn_prefill_window")
+
+
+def lazyattn_decode_window(pool: int, batch: lazyattn_batch, q, k_new, v_new, out, window: int, sinks: int, workspace,
+                           workspace_bytes: int, stream=None):
+    """lazyattn_decode under the rule of lazyattn_prefill_window."""
+    _dense("lazyattn_decode_window", q, k_new, v_new, out)
+    _check(lib.lazyattn_decode_window(pool, ctypes.byref(batch), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out), window,
+                                      sinks, _ptr(workspace), workspace_bytes, _stream(stream)), "lazyattn_decode_window")
+
+
+def lazyattn_prefill_mass(pool: int, batch: lazyattn_batch, q, mass_in, mass_out, decay: float, workspace,
+                          workspace_bytes: int, stream=None):
+    """mass_out = decay * mass_in + the attention weight each cached token gets from
+    the rows of q (float32 [entries][n_kv_heads][16]; mass_in None: nothing yet)."""
+    _dense("lazyattn_prefill_mass", q)
+    _dense("lazyattn_prefill_mass", mass_in, mass_out, dtype=("float32",))
+    _check(lib.lazyattn_prefill_mass(pool, ctypes.byref(batch), _ptr(q), _ptr(mass_in), _ptr(mass_out), decay,
+                                     _ptr(workspace), workspace_bytes, _stream(stream)), "lazyattn_prefill_mass")
+
+
+def lazyattn_decode_mass(pool: int, batch: lazyattn_batch, q, k_new, v_new, out, mass_in, mass_out, decay: float,
+                         workspace, workspace_bytes: int, stream=None):
+    """lazyattn_decode and the attention weight of its step, as in lazyattn_prefill_mass."""
+    _dense("lazyattn_decode_mass", q, k_new, v_new, out)
+    _dense("lazyattn_decode_mass", mass_in, mass_out, dtype=("float32",))
+    _check(lib.lazyattn_decode_mass(pool, ctypes.byref(batch), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out),
+                                    _ptr(mass_in), _ptr(mass_out), decay, _ptr(workspace), workspace_bytes,
+                                    _stream(stream)), "lazyattn_decode_mass")
+
+
+def lazyattn_evict(pool: int, batch: lazyattn_batch, mass, budget: int, sinks: int, recent: int, dst_entries,
+                   dst_offsets, kept, dst_mass=None, stream=None):
+    """Copy the `budget` tokens each KV head keeps (first `sinks`, last `recent`, the
+    rest by mass) into the pages of dst_entries, at positions 0, 1, ..."""
+    _dense("lazyattn_evict", mass, dst_mass, dtype=("float32",))
+    _dense("lazyattn_evict", dst_offsets, kept, dtype=("int32",))
+    _dense("lazyattn_evict", dst_entries, dtype=("int64", "uint64"))
+    _check(lib.lazyattn_evict(pool, ctypes.byref(batch), _ptr(mass), budget, sinks, recent, _ptr(dst_entries),
+                              _ptr(dst_offsets), _ptr(kept), _ptr(dst_mass), _stream(stream)), "lazyattn_evict")
 
 
 def lazyattn_materialize(pool: int, batch: lazyattn_batch, dst_entries, stream=None):

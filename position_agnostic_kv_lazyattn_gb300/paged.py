@@ -191,6 +191,46 @@ class Batch:
         if rc != 0:
             raise L.LazyAttnError(rc, f"block table of request {bad}")
 
+    def evict(self, pool: "DevicePool", mass: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0,
+              reserve: int = 1, stream=None):
+        """Cut every request's cache down to `budget` tokens per KV head
+        (lazyattn_evict by `mass`, float32 [entries][n_kv_heads][16]): takes
+        ceil(budget / 16) + reserve fresh, writable pages per request from the pool, and
+        returns (the new Batch, kept positions int32 [R][n_kv_heads][budget],
+        the new batch's mass). Later decode steps append into the reserved
+        room. The old pages are still the caller's to free. Reads the new table back to the
+        host, so it waits for the stream."""
+        if stream is not None:
+            stream = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+            with torch.cuda.stream(stream):
+                return self.evict(pool, mass, budget, sinks, recent, reserve)
+        R, per = self.num_requests, -(-budget // PAGE_SIZE) + reserve
+        device = self.entries.device
+        if tuple(mass.shape[1:]) != (pool.n_kv_heads, PAGE_SIZE) or mass.shape[0] < int(self.offsets_host[-1]):
+            raise ValueError("mass must be [entries][n_kv_heads][16] of this batch's table")
+        pages = pool.alloc_pages(R * per)
+        try:
+            dst = torch.from_numpy(pack_entries(pages, [0] * len(pages), [0] * len(pages), [1] * len(pages))
+                                   .view(np.int64).copy()).to(device)
+            offsets = (np.arange(R + 1) * per).astype(np.int32)
+            dst_offsets = torch.from_numpy(offsets).to(device)
+            kept = torch.empty((R, pool.n_kv_heads, budget), dtype=torch.int32, device=device)
+            new_mass = torch.empty((R * per, pool.n_kv_heads, PAGE_SIZE), dtype=torch.float32, device=device)
+            L.lazyattn_evict(pool.handle, self.c, mass, budget, sinks, recent, dst, dst_offsets, kept, new_mass)
+        except Exception:
+            pool.free_pages(pages)
+            raise
+        b = Batch.__new__(Batch)
+        b.num_requests, b.max_entries, b.offsets_host, b.flags, b.plan = R, per, offsets, 0, None
+        b.entries, b.entry_offsets = dst, dst_offsets
+        b.entries_host = dst.cpu().numpy().view(np.uint64)
+        b.delta_host = np.zeros(max(1, R * per), np.int32)
+        b.entry_delta = torch.from_numpy(b.delta_host).to(device)
+        b.q_offsets = b.q_start = None
+        b.total_q = b.max_q_len = 0
+        b.c = L.make_batch(R, per, b.entries, b.entry_offsets, entry_delta=b.entry_delta)
+        return b, kept, new_mass
+
     def with_entries(self, entries_host: np.ndarray, flags: int, device="cuda") -> "Batch":
         """Same requests and query layout, another entry array (e.g. materialised pages)."""
         b = Batch.__new__(Batch)

@@ -1,0 +1,631 @@
+"""GPU tests of windowed attention, attention mass and eviction against the
+64-bit definitions of tests/cache_common.py, on every key layout and position
+encoding, with ragged tables and the sizes where such kernels go wrong."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from tests.cache_common import MODES, Scenario, attend, check_mass
+from tests.gpu_common import compare
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import __graft_entry__
+    __graft_entry__.build()
+    import position_agnostic_kv_lazyattn_gb300 as L
+    return L
+
+
+def workspace(L, s, op, window=None, sinks=0):
+    n = (L.lazyattn_workspace_size(s.pool.handle, op, s.batch.c) if window is None else
+         L.lazyattn_window_workspace_size(s.pool.handle, op, s.batch.c, window, sinks))
+    assert n > 0
+    return torch.zeros(n, dtype=torch.uint8, device="cuda"), n
+
+
+def prefill_window(L, s, window, sinks):
+    ws, n = workspace(L, s, L.LAZYATTN_OP_PREFILL, window, sinks)
+    out = s.empty(max(1, s.batch.total_q), s.hq, s.d)
+    L.lazyattn_prefill_window(s.pool.handle, s.batch.c, s.dev(s.q), out, window, sinks, ws, n)
+    return out.float().cpu().numpy()
+
+
+def check_prefill_window(L, s, window, sinks):
+    got = prefill_window(L, s, window, sinks)
+    for r, rows in enumerate(s.rows):
+        if not rows:
+            continue
+        want, _, _ = attend(s.spec, s.q[s.row_slice(r)], s.k[r], s.v[r], s.starts[r] + np.arange(rows), s.pos[r], window, sinks)
+        compare(got[s.row_slice(r)], want, s.dtype)
+    assert s.pool.device_status() == 0
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_prefill_window_modes(L, mode):
+    s = Scenario(L, [([70, 33], 40, 40), ([5, 100, 130], 17, 9), ([], 30, 30)], mode)
+    check_prefill_window(L, s, 50, 3)
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (8, 2), (8, 1)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (17, 16), (100, 5), (128, 128), (1000, 0), (2**31 - 1, 0)])
+def test_prefill_window_sizes(L, hq, hkv, window, sinks):
+    """Windows of one token, of a page and around it, past the whole cache; odd lengths, a request without rows."""
+    s = Scenario(L, [([260, 1, 16], 129, 129), ([40], 8, 0), ([], 1, 1), ([17, 300], 300, 130)], hq=hq, hkv=hkv, seed=1)
+    check_prefill_window(L, s, window, sinks)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (20, 3), (10000, 0)])
+def test_prefill_window_fp32(L, d, window, sinks):
+    s = Scenario(L, [([70, 33], 40, 40), ([5, 100, 130], 17, 9), ([], 1, 1)], dtype="f32", hq=4, hkv=2, d=d, q_scale=1.0)
+    check_prefill_window(L, s, window, sinks)
+
+
+def test_prefill_window_long(L):
+    """Many tiles, most of them skipped: rows in the middle and at the end of a long sequence."""
+    s = Scenario(L, [([900] * 9, 200, 200), ([500, 500], 90, 90)], seed=2)
+    for window, sinks in [(64, 4), (700, 0), (3000, 20)]:
+        check_prefill_window(L, s, window, sinks)
+
+
+def test_prefill_window_of_everything_is_prefill(L):
+    s = Scenario(L, [([300, 33], 90, 90)], seed=3)
+    out = s.empty(90, s.hq, s.d)
+    L.lazyattn_prefill(s.pool.handle, s.batch.c, s.dev(s.q), out)
+    got = prefill_window(L, s, 100000, 0)
+    np.testing.assert_array_equal(got, out.float().cpu().numpy())
+
+
+def test_prefill_window_rows_that_see_nothing(L):
+    """Positions with gaps: rows whose window holds no token get zeros; entries out of order and empty ones."""
+    s = Scenario(L, [([20, 50], 30, 30)], seed=4, gap=100)
+    b = s.batch
+    order = np.r_[np.arange(s.n_entries())[::-1]]
+    ent = b.entries_host[order]
+    b2 = b.with_entries(ent, 0)
+    q = s.normal(64, s.hq, s.d) * 2
+    start = 60                                     # positions 60..123: documents at 0..19 and 120..169
+    off = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    qs = torch.tensor([start], dtype=torch.int32, device="cuda")
+    c = L.lazyattn.make_batch(1, b.max_entries, b2.entries, b.entry_offsets, off, qs, 64, 64)
+    out = s.empty(64, s.hq, s.d)
+    L.lazyattn_prefill_window(s.pool.handle, c, s.dev(q), out, 30, 0)
+    want, _, _ = attend(s.spec, q, s.k[0], s.v[0], start + np.arange(64), s.pos[0], 30, 0)
+    assert np.all(want[:60] == 0) and np.any(want[60:] != 0)
+    got = out.float().cpu().numpy()
+    assert np.all(got[:60] == 0)
+    compare(got, want, "bf16")
+
+
+def decode_state(s):
+    return [k.copy() for k in s.k], [v.copy() for v in s.v], [p.copy() for p in s.pos]
+
+
+def step_inputs(s, R):
+    return s.normal(R, s.hq, s.d) * 2, s.normal(R, s.hkv, s.d), s.normal(R, s.hkv, s.d)
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_decode_window_modes(L, mode):
+    s = Scenario(L, [([70, 33], 40, 0), ([5, 100, 130], 15, 0), ([], 30, 0)], mode)
+    check_decode_window(L, s, 50, 3, 3)
+
+
+def check_decode_window(L, s, window, sinks, steps):
+    R = len(s.rows)
+    ws, n = workspace(L, s, L.LAZYATTN_OP_DECODE, window, sinks)
+    k, v, pos = decode_state(s)
+    for _ in range(steps):
+        q, kn, vn = step_inputs(s, R)
+        out = s.empty(R, s.hq, s.d)
+        L.lazyattn_decode_window(s.pool.handle, s.batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, window, sinks, ws, n)
+        got = out.float().cpu().numpy()
+        for r in range(R):
+            m = int(pos[r][-1]) + 1 if len(pos[r]) else 0
+            k[r], v[r], pos[r] = np.r_[k[r], kn[r][None]], np.r_[v[r], vn[r][None]], np.r_[pos[r], m]
+            want, _, _ = attend(s.spec, q[r][None], k[r], v[r], [m], pos[r], window, sinks)
+            compare(got[r], want[0], s.dtype)
+            if window == 1 and sinks == 0:   # its own value, bit for bit
+                np.testing.assert_array_equal(got[r], np.repeat(vn[r], s.hq // s.hkv, 0))
+    assert s.pool.device_status() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 2), (8, 2), (8, 1), (10, 2)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (17, 16), (100, 5), (1000, 0), (2**31 - 1, 7)])
+def test_decode_window_sizes(L, hq, hkv, window, sinks):
+    s = Scenario(L, [([260, 1, 16], 129, 0), ([], 0, 0), ([], 1, 0), ([17, 300], 300, 0), ([], 16, 0)], hq=hq, hkv=hkv, seed=5)
+    check_decode_window(L, s, window, sinks, 2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_window_fp32(L, d):
+    s = Scenario(L, [([70, 33], 40, 0), ([5, 400, 130], 17, 0), ([], 0, 0)], dtype="f32", hq=4, hkv=2, d=d)
+    check_decode_window(L, s, 90, 3, 2)
+
+
+@pytest.mark.parametrize("window,sinks", [(64, 4), (2500, 0), (5000, 300)])
+def test_decode_window_long(L, window, sinks):
+    s = Scenario(L, [([900] * 9, 200, 0), ([500, 500], 90, 0)], seed=6, hq=32, hkv=8)
+    check_decode_window(L, s, window, sinks, 1)
+
+
+def test_windows_do_not_read_what_they_hide(L):
+    """Pages none of whose tokens is visible may hold anything."""
+    s = Scenario(L, [([320, 320], 64, 20)], seed=7)
+    hidden = [p for p in s.segments[0][0].pages[1:]] + [p for p in s.segments[0][1].pages[:10]]
+    at = torch.tensor(hidden, device="cuda")
+    s.pool.k_pool[at] = float("nan")
+    s.pool.v_pool[at] = float("inf")
+    check_prefill_window(L, s, 100, 16)
+    check_decode_window(L, s, 100, 16, 1)
+
+
+def test_decode_window_without_a_slot(L):
+    """A request with no writable free slot: zeros, reported; the others are served."""
+    s = Scenario(L, [([40], 16, 0), ([20], 5, 0)], spare=0, seed=8)
+    ws, n = workspace(L, s, L.LAZYATTN_OP_DECODE, 30, 2)
+    q, kn, vn = step_inputs(s, 2)
+    out = s.empty(2, s.hq, s.d)
+    L.lazyattn_decode_window(s.pool.handle, s.batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, 30, 2, ws, n)
+    got = out.float().cpu().numpy()
+    assert np.all(got[0] == 0)
+    want, _, _ = attend(s.spec, q[1][None], np.r_[s.k[1], kn[1][None]], np.r_[s.v[1], vn[1][None]], [25], np.arange(26), 30, 2)
+    compare(got[1], want[0], "bf16")
+    assert s.pool.device_status() == L.LAZYATTN_ENODECODE
+
+
+# ------------------------------------------------------------------------------------------------ mass
+
+def check_prefill_mass(L, s, decay, old):
+    rng = np.random.default_rng(11)
+    ws, n = workspace(L, s, L.LAZYATTN_OP_PREFILL_MASS)
+    before = [rng.random((len(p), s.hkv)).astype(np.float32) for p in s.pos] if old else None
+    mass_in = torch.from_numpy(s.mass_of(before).astype(np.float32)).cuda() if old else None
+    out = torch.full((s.n_entries() + 1, s.hkv, 16), float("nan"), device="cuda")
+    q = s.dev(s.q) if len(s.q) else None
+    L.lazyattn_prefill_mass(s.pool.handle, s.batch.c, q, mass_in, out, decay, ws, n)
+    assert bool(torch.isnan(out[-1]).all())                                    # behind the table: left alone
+    want, reach = [], 0.0
+    for r, rows in enumerate(s.rows):
+        _, w, top = attend(s.spec, s.q[s.row_slice(r)], s.k[r], s.v[r], s.starts[r] + np.arange(rows), s.pos[r])
+        want.append(w + (np.float32(decay) * before[r].astype(np.float64) if old else 0.0))
+        reach = max(reach, top)
+    check_mass(out[:-1].cpu().numpy(), s.mass_of(want), reach, s.mode in ("prerotated", "doc_local"))
+    again = torch.full_like(out, float("nan"))
+    L.lazyattn_prefill_mass(s.pool.handle, s.batch.c, q, mass_in, again, decay, ws, n)
+    assert torch.equal(out[:-1], again[:-1])                                   # equal calls, equal bits
+    if old:                                                                    # in place
+        L.lazyattn_prefill_mass(s.pool.handle, s.batch.c, q, mass_in, mass_in, decay, ws, n)
+        assert torch.equal(out[:-1], mass_in)
+    assert s.pool.device_status() == 0
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_prefill_mass_modes(L, mode):
+    s = Scenario(L, [([70, 33], 40, 40), ([5, 100, 130], 17, 9), ([], 30, 30)], mode, seed=12)
+    check_prefill_mass(L, s, 0.5, True)
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 2), (8, 2), (8, 1), (10, 2)])
+@pytest.mark.parametrize("rows", [1, 3, 64, 130, 300])
+def test_prefill_mass_sizes(L, hq, hkv, rows):
+    s = Scenario(L, [([260, 1, 16], rows, rows), ([40], 8, 0), ([], 1, 1), ([17, 300], 300, max(1, rows // 2))], hq=hq, hkv=hkv,
+                 seed=13)
+    check_prefill_mass(L, s, 1.0, rows != 3)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_mass_fp32(L, d):
+    s = Scenario(L, [([70, 33], 40, 40), ([5, 100, 130], 17, 9), ([], 1, 1)], dtype="f32", hq=4, hkv=2, d=d, seed=14)
+    check_prefill_mass(L, s, 0.9, True)
+
+
+def test_prefill_mass_long(L):
+    s = Scenario(L, [([900] * 9, 100, 100), ([500, 500], 90, 33)], seed=15, hq=8, hkv=2)
+    check_prefill_mass(L, s, 1.0, False)
+
+
+def test_prefill_mass_without_rows(L):
+    """No row at all: the weights fade, nothing is added."""
+    s = Scenario(L, [([70, 33], 40, 0), ([], 3, 0)], seed=16)
+    s.batch.q_offsets = torch.zeros(3, dtype=torch.int32, device="cuda")
+    s.batch.q_start = torch.zeros(2, dtype=torch.int32, device="cuda")
+    s.batch.c.q_offsets, s.batch.c.q_start = s.batch.q_offsets.data_ptr(), s.batch.q_start.data_ptr()
+    check_prefill_mass(L, s, 0.25, True)
+
+
+def check_decode_mass(L, s, decay, steps, spare_mass=True):
+    R = len(s.rows)
+    ws, n = workspace(L, s, L.LAZYATTN_OP_DECODE_MASS)
+    k, v, pos = decode_state(s)
+    mass = torch.zeros(s.n_entries() + 1, s.hkv, 16, device="cuda") if spare_mass else None
+    total = [np.zeros((len(p), s.hkv)) for p in pos]
+    reach = 0.0
+    for _ in range(steps):
+        q, kn, vn = step_inputs(s, R)
+        out = s.empty(R, s.hq, s.d)
+        new = torch.full((s.n_entries() + 1, s.hkv, 16), float("nan"), device="cuda") if not spare_mass else mass
+        L.lazyattn_decode_mass(s.pool.handle, s.batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, mass, new, decay, ws, n)
+        got = out.float().cpu().numpy()
+        for r in range(R):
+            m = int(pos[r][-1]) + 1 if len(pos[r]) else 0
+            k[r], v[r], pos[r] = np.r_[k[r], kn[r][None]], np.r_[v[r], vn[r][None]], np.r_[pos[r], m]
+            want, w, top = attend(s.spec, q[r][None], k[r], v[r], [m], pos[r], causal=False)
+            reach = max(reach, top)
+            compare(got[r], want[0], s.dtype)
+            total[r] = (decay * np.r_[total[r], np.zeros((1, s.hkv))] if spare_mass else 0.0) + w
+        check_mass(new[:-1].cpu().numpy(), s.mass_of(total), reach, s.mode in ("prerotated", "doc_local"))
+    assert s.pool.device_status() == 0
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_decode_mass_modes(L, mode):
+    s = Scenario(L, [([70, 33], 40, 0), ([5, 100, 130], 15, 0), ([], 30, 0)], mode, seed=17)
+    check_decode_mass(L, s, 0.5, 3)
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 2), (8, 2), (8, 1), (10, 2)])
+@pytest.mark.parametrize("decay,old", [(1.0, True), (0.0, False)])
+def test_decode_mass_sizes(L, hq, hkv, decay, old):
+    s = Scenario(L, [([260, 1, 16], 129, 0), ([], 0, 0), ([], 1, 0), ([17, 300], 300, 0), ([], 16, 0)], hq=hq, hkv=hkv, seed=18)
+    check_decode_mass(L, s, decay, 2, old)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_mass_fp32(L, d):
+    s = Scenario(L, [([70, 33], 40, 0), ([5, 400, 130], 17, 0), ([], 0, 0)], dtype="f32", hq=4, hkv=2, d=d, seed=19)
+    check_decode_mass(L, s, 1.0, 2)
+
+
+def test_decode_mass_long(L):
+    s = Scenario(L, [([900] * 9, 200, 0), ([500, 500], 90, 0)], seed=20, hq=32, hkv=8)
+    check_decode_mass(L, s, 1.0, 2)
+
+
+def test_decode_mass_output_is_decode(L):
+    """The same output as a plain decode step, to the bounds of both."""
+    outs = []
+    for which in range(2):
+        s = Scenario(L, [([260, 1, 16], 129, 0), ([17, 300], 300, 0)], seed=21)
+        q, kn, vn = step_inputs(s, 2)
+        out = s.empty(2, s.hq, s.d)
+        if which:
+            ws, n = workspace(L, s, L.LAZYATTN_OP_DECODE_MASS)
+            mass = torch.empty(s.n_entries(), s.hkv, 16, device="cuda")
+            L.lazyattn_decode_mass(s.pool.handle, s.batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, None, mass, 1.0, ws, n)
+        else:
+            ws, n = workspace(L, s, L.LAZYATTN_OP_DECODE)
+            L.lazyattn_decode(s.pool.handle, s.batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, ws, n)
+        outs.append(out.float().cpu().numpy())
+    compare(outs[1], outs[0], "bf16")
+
+
+def test_decode_mass_without_a_slot(L):
+    """A request with no writable free slot keeps its mass, unfaded."""
+    s = Scenario(L, [([40], 16, 0), ([20], 5, 0)], spare=0, seed=22)
+    ws, n = workspace(L, s, L.LAZYATTN_OP_DECODE_MASS)
+    q, kn, vn = step_inputs(s, 2)
+    out = s.empty(2, s.hq, s.d)
+    before = s.mass_of([np.full((56, s.hkv), 0.75), np.full((25, s.hkv), 0.5)]).astype(np.float32)
+    mass = torch.from_numpy(before).cuda()
+    L.lazyattn_decode_mass(s.pool.handle, s.batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, mass, mass, 0.5, ws, n)
+    got = mass.cpu().numpy()
+    np.testing.assert_array_equal(got[:4], before[:4])
+    assert np.all(out[0].float().cpu().numpy() == 0)
+    _, w, reach = attend(s.spec, q[1][None], np.r_[s.k[1], kn[1][None]], np.r_[s.v[1], vn[1][None]], [25], np.arange(26))
+    check_mass(got, s.mass_of([np.full((56, s.hkv), 0.75), w + 0.25 * (np.arange(26) < 25)[:, None]]), reach)
+    assert s.pool.device_status() == L.LAZYATTN_ENODECODE
+
+
+# ------------------------------------------------------------------------------------------------ eviction
+
+def kept_tokens(w, budget, sinks, recent):
+    """Token numbers one head keeps, from its tokens' weights: sorted by (weight, NaN least; earlier first)."""
+    n = len(w)
+    if n <= budget:
+        return np.arange(n)
+    fixed = np.r_[np.arange(min(sinks, n)), np.arange(max(min(sinks, n), n - recent), n)]
+    free = np.setdiff1d(np.arange(n), fixed)
+    key = np.where(np.isnan(w), -np.inf, w)
+    nan = np.isnan(w)
+    best = sorted(free, key=lambda t: (nan[t], -key[t], t))[: budget - len(fixed)]
+    return np.sort(np.r_[fixed, best]).astype(int)
+
+
+def check_evict(L, s, weights, budget, sinks, recent, spare=1, dst_mass=True):
+    R = len(s.rows)
+    per = -(-budget // 16) + spare
+    pages = np.array(s.pool.alloc_pages(R * per))
+    wr = np.zeros(R * per, int)
+    wr[1::2] = 1
+    dst = torch.from_numpy(L.pack_entries(pages, np.full(R * per, 77), np.full(R * per, 9), wr).view(np.int64).copy()).cuda()
+    off = torch.arange(R + 1, dtype=torch.int32, device="cuda") * per
+    mass = torch.from_numpy(s.mass_of(weights).astype(np.float32)).cuda()
+    kept = torch.full((R + 1, s.hkv, budget), -7, dtype=torch.int32, device="cuda")
+    out_mass = torch.full((R * per + 1, s.hkv, 16), float("nan"), device="cuda") if dst_mass else None
+    at = torch.from_numpy(pages).cuda()
+    s.pool.k_pool[at] = 3.0
+    s.pool.v_pool[at] = 3.0
+    k0, v0 = s.pool.k_pool.clone(), s.pool.v_pool.clone()
+    L.lazyattn_evict(s.pool.handle, s.batch.c, mass, budget, sinks, recent, dst, off, kept, out_mass)
+    assert s.pool.device_status() == 0
+    kept, dst_h = kept.cpu().numpy(), dst.cpu().numpy().view(np.uint64)
+    assert np.all(kept[R] == -7)
+    want_k, want_v = k0.clone(), v0.clone()
+    want_mass = np.zeros((R * per, s.hkv, 16), np.float32)
+    ent = s.batch.entries.cpu().numpy().view(np.uint64)
+    for r in range(R):
+        toks = oracle.resolve_entries(ent[s.batch.offsets_host[r]:s.batch.offsets_host[r + 1]])
+        count = min(len(toks), budget)
+        for i in range(per):
+            assert oracle.unpack_entry(int(dst_h[r * per + i])) == (pages[r * per + i], 16 * i, max(0, min(16, count - 16 * i)),
+                                                                      wr[r * per + i])
+        for h in range(s.hkv):
+            ids = kept_tokens(np.asarray(weights[r])[:, h].astype(np.float32), budget, sinks, recent)
+            assert len(ids) == count
+            want = np.full(budget, -1)
+            want[:count] = [toks[t][2] for t in ids]
+            np.testing.assert_array_equal(kept[r, h], want)
+            for j in range(-(-count // 16) * 16):
+                p, slot = int(pages[r * per + j // 16]), j % 16
+                if j < count:
+                    src = toks[ids[j]]
+                    want_k[p, h, slot], want_v[p, h, slot] = k0[src[0], h, src[1]], v0[src[0], h, src[1]]
+                    want_mass[r * per + j // 16, h, slot] = weights[r][ids[j], h]
+                else:
+                    want_k[p, h, slot] = want_v[p, h, slot] = 0
+    assert torch.equal(s.pool.k_pool, want_k) and torch.equal(s.pool.v_pool, want_v)   # and nothing else was written
+    if dst_mass:
+        np.testing.assert_array_equal(out_mass[:-1].cpu().numpy(), want_mass)
+        assert bool(torch.isnan(out_mass[-1]).all())
+
+
+def weights_of(s, kind, rng):
+    ws = []
+    for p in s.pos:
+        w = rng.standard_normal((len(p), s.hkv)).astype(np.float32)
+        if kind == "ties":
+            w = np.round(np.exp(w)).astype(np.float32)
+        if kind == "equal":
+            w[:] = 0.25
+        if kind == "odd":   # NaN, infinities, both zeros, denormals
+            w = np.array([np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-42, -1e-42, 1.0, -1.0], np.float32)[rng.integers(0, 9, w.shape)]
+        ws.append(w)
+    return ws
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties", "equal", "odd"])
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (1, 0, 1), (16, 0, 0), (50, 4, 10), (33, 33, 0), (100, 0, 100), (500, 3, 9)])
+def test_evict(L, kind, budget, sinks, recent):
+    s = Scenario(L, [([70, 33], 40, 0), ([5, 100, 130], 17, 0), ([], 1, 0), ([], 0, 0)], seed=23, extra=4 * 34)
+    check_evict(L, s, weights_of(s, kind, np.random.default_rng(24)), budget, sinks, recent)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d,mode", [("f32", 4, 2, 64, "rope"), ("f32", 4, 2, 128, "rope"), ("bf16", 8, 8, 128, "alibi"),
+                                                 ("bf16", 6, 3, 128, "interleaved"), ("bf16", 8, 1, 128, "yarn")])
+def test_evict_pools(L, dtype, hq, hkv, d, mode):
+    s = Scenario(L, [([70, 33], 40, 0), ([5, 100, 130], 17, 0)], mode, dtype, hq, hkv, d, seed=25, extra=40)
+    check_evict(L, s, weights_of(s, "normal", np.random.default_rng(26)), 61, 4, 10, dst_mass=False)
+
+
+@pytest.mark.parametrize("n_docs,budget", [(9, 700), (40, 3000), (150, 40)])
+def test_evict_long(L, n_docs, budget):
+    s = Scenario(L, [([1000 - 7 * (j % 5) for j in range(n_docs)], 20, 0), ([30], 5, 0)], hq=2, hkv=2, seed=27, extra=2 * 200)
+    check_evict(L, s, weights_of(s, "ties", np.random.default_rng(28)), budget, 4, 33)
+
+
+def test_evict_refuses_bad_tables_on_the_device(L):
+    """Entries that go down in position, a page out of range, too few new entries, a new page out of range: that request
+    keeps nothing and is reported; the other request is served."""
+    for fault in ["order", "page", "few", "new page"]:
+        s = Scenario(L, [([40, 30], 20, 0), ([50], 9, 0)], seed=29, extra=8)
+        ent = s.batch.entries_host.copy()
+        if fault == "order":
+            ent[[0, 1]] = ent[[1, 0]]
+        if fault == "page":
+            ent[1] = (ent[1] & ~np.uint64(0xFFFFFFFF)) | np.uint64(s.pool.num_pages)
+        b = s.batch.with_entries(ent, 0)
+        pages = np.array(s.pool.alloc_pages(4))
+        if fault == "new page":
+            pages[1] = s.pool.num_pages + 5
+        offs = [0, 1, 3] if fault == "few" else [0, 2, 4]
+        dst = torch.from_numpy(L.pack_entries(pages, [0] * 4, [0] * 4, [1] * 4).view(np.int64).copy()).cuda()
+        off = torch.tensor(offs, dtype=torch.int32, device="cuda")
+        kept = torch.zeros(2, s.hkv, 20, dtype=torch.int32, device="cuda")
+        mass = torch.ones(s.n_entries(), s.hkv, 16, device="cuda")
+        dm = torch.full((4, s.hkv, 16), float("nan"), device="cuda")
+        k0 = s.pool.k_pool.clone()
+        L.lazyattn_evict(s.pool.handle, b.c, mass, 20, 1, 2, dst, off, kept, dm)
+        assert s.pool.device_status() == L.LAZYATTN_ERANGE, fault
+        kept, dst = kept.cpu().numpy(), dst.cpu().numpy().view(np.uint64)
+        assert np.all(kept[0] == -1) and np.all(kept[1] >= 0)
+        assert all(oracle.unpack_entry(int(e))[2] == 0 for e in dst[:offs[1]])
+        assert sum(oracle.unpack_entry(int(e))[2] for e in dst[offs[1]:offs[2]]) == 20
+        assert np.all(dm.cpu().numpy()[:offs[1]] == 0)
+        touched = (s.pool.k_pool != k0).flatten(1).any(1).cpu().numpy().nonzero()[0]
+        assert set(touched) <= set(pages[offs[1]:offs[2]])
+
+
+# ------------------------------------------------------------------------------------------------ refusals
+
+def test_refusals(L):
+    s = Scenario(L, [([40, 30], 20, 8)], seed=30, extra=4)
+    q, out = s.dev(s.q), s.empty(8, s.hq, s.d)
+    q1, k1, v1 = (s.dev(x) for x in step_inputs(s, 1))
+    o1 = s.empty(1, s.hq, s.d)
+    mass = torch.zeros(s.n_entries(), s.hkv, 16, device="cuda")
+    dst = torch.from_numpy(L.pack_entries(s.pool.alloc_pages(2), [0] * 2, [0] * 2, [1] * 2).view(np.int64).copy()).cuda()
+    off = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    kept = torch.full((1, s.hkv, 20), -7, dtype=torch.int32, device="cuda")
+    h, c = s.pool.handle, s.batch.c
+    wsw, nw = workspace(L, s, L.LAZYATTN_OP_DECODE, 8, 0)
+    wsp, npm = workspace(L, s, L.LAZYATTN_OP_PREFILL_MASS)
+    wsd, ndm = workspace(L, s, L.LAZYATTN_OP_DECODE_MASS)
+    EINVAL, EWS = L.LAZYATTN_EINVAL, L.LAZYATTN_EWORKSPACE
+    odd = torch.zeros(4 * mass.numel(), device="cuda")[1:1 + mass.numel()]
+    nan = float("nan")
+    calls = [
+        (EINVAL, lambda: L.lazyattn_prefill_window(h, c, q, out, 0, 0)),
+        (EINVAL, lambda: L.lazyattn_prefill_window(h, c, q, out, -5, 0)),
+        (EINVAL, lambda: L.lazyattn_prefill_window(h, c, q, out, 8, -1)),
+        (EINVAL, lambda: L.lazyattn_prefill_window(h, c, None, out, 8, 0)),
+        (EINVAL, lambda: L.lazyattn_prefill_window(h, c, q, None, 8, 0)),
+        (EINVAL, lambda: L.lazyattn_prefill_window(h, c, q[:, :, ::2], out, 8, 0)),
+        (EINVAL, lambda: L.lazyattn_decode_window(h, c, q1, k1, v1, o1, 0, 0, wsw, nw)),
+        (EINVAL, lambda: L.lazyattn_decode_window(h, c, q1, None, v1, o1, 8, 0, wsw, nw)),
+        (EINVAL, lambda: L.lazyattn_decode_window(h, c, q1, k1, v1, o1, 8, 0, None, nw)),
+        (EINVAL, lambda: L.lazyattn_decode_window(h, c, q1, k1, v1, o1, 8, 0, wsw.data_ptr() + 16, nw)),
+        (EWS, lambda: L.lazyattn_decode_window(h, c, q1, k1, v1, o1, 8, 0, wsw, nw - 1)),
+        (EINVAL, lambda: L.lazyattn_prefill_mass(h, c, q, mass, mass, 1.5, wsp, npm)),
+        (EINVAL, lambda: L.lazyattn_prefill_mass(h, c, q, mass, mass, -0.1, wsp, npm)),
+        (EINVAL, lambda: L.lazyattn_prefill_mass(h, c, q, mass, mass, nan, wsp, npm)),
+        (EINVAL, lambda: L.lazyattn_prefill_mass(h, c, q, mass, None, 1.0, wsp, npm)),
+        (EINVAL, lambda: L.lazyattn_prefill_mass(h, c, None, mass, mass, 1.0, wsp, npm)),
+        (EINVAL, lambda: L.lazyattn_prefill_mass(h, c, q, odd, mass, 1.0, wsp, npm)),
+        (EINVAL, lambda: L.lazyattn_prefill_mass(h, c, q, mass.double(), mass, 1.0, wsp, npm)),
+        (EWS, lambda: L.lazyattn_prefill_mass(h, c, q, mass, mass, 1.0, wsp, npm - 1)),
+        (EINVAL, lambda: L.lazyattn_decode_mass(h, c, q1, k1, v1, o1, mass, mass, nan, wsd, ndm)),
+        (EINVAL, lambda: L.lazyattn_decode_mass(h, c, q1, k1, v1, None, mass, mass, 1.0, wsd, ndm)),
+        (EWS, lambda: L.lazyattn_decode_mass(h, c, q1, k1, v1, o1, mass, mass, 1.0, wsd, ndm - 1)),
+        (EINVAL, lambda: L.lazyattn_evict(h, c, mass, 0, 0, 0, dst, off, kept)),
+        (EINVAL, lambda: L.lazyattn_evict(h, c, mass, 20, -1, 0, dst, off, kept)),
+        (EINVAL, lambda: L.lazyattn_evict(h, c, mass, 20, 11, 10, dst, off, kept)),
+        (EINVAL, lambda: L.lazyattn_evict(h, c, mass, 20, 2**31 - 1, 2**31 - 1, dst, off, kept)),
+        (EINVAL, lambda: L.lazyattn_evict(h, c, None, 20, 1, 1, dst, off, kept)),
+        (EINVAL, lambda: L.lazyattn_evict(h, c, mass, 20, 1, 1, dst, off.long(), kept)),
+        (EINVAL, lambda: L.lazyattn_evict(h, c, mass, 20, 1, 1, None, off, kept)),
+        (EINVAL, lambda: L.lazyattn_evict(h, c, mass, 20, 1, 1, dst, off, None)),
+    ]
+    table = s.batch.entries.clone()
+    for i, (code, call) in enumerate(calls):
+        with pytest.raises(L.LazyAttnError) as e:
+            call()
+        assert e.value.code == code, i
+    torch.cuda.synchronize()
+    assert torch.equal(table, s.batch.entries) and bool((kept == -7).all()) and bool(torch.isnan(out).all())
+    assert L.lazyattn_window_workspace_size(h, L.LAZYATTN_OP_DECODE, c, 0, 0) == 0
+    assert L.lazyattn_window_workspace_size(h, L.LAZYATTN_OP_PREFILL_MASS, c, 8, 0) == 0
+
+
+@pytest.mark.parametrize("mode", ["doc_local", "prerotated"])
+def test_evict_refuses_keys_turned_to_their_place(L, mode):
+    s = Scenario(L, [([40, 30], 20, 0)], mode, seed=31, extra=4)
+    z = torch.zeros(64, dtype=torch.int64, device="cuda")
+    with pytest.raises(L.LazyAttnError) as e:
+        L.lazyattn_evict(s.pool.handle, s.batch.c, z.float(), 20, 1, 1, z, z.int(), z.int())
+    assert e.value.code == L.LAZYATTN_EINVAL
+
+
+# ------------------------------------------------------------------------------------------------ together
+
+def test_a_cache_kept_small(L):
+    """A prompt under a window, its last rows observing the cache, the cache cut down, decode steps that go on
+    observing, a second cut, and a windowed step: each step against the 64-bit definition on the tokens then held."""
+    s = Scenario(L, [([300, 150], 64, 64), ([200, 77, 130], 40, 40)], seed=32, hq=8, hkv=2, extra=200)
+    R, hkv = 2, s.hkv
+    check_prefill_window(L, s, 128, 4)
+    ws, n = workspace(L, s, L.LAZYATTN_OP_PREFILL_MASS)
+    mass = torch.empty(s.n_entries(), hkv, 16, device="cuda")
+    L.lazyattn_prefill_mass(s.pool.handle, s.batch.c, s.dev(s.q), None, mass, 1.0, ws, n)
+    # per request and head: the tokens held, in order
+    held = [[(s.k[r][:, h], s.v[r][:, h]) for h in range(hkv)] for r in range(R)]
+    batch, free0 = s.batch, s.pool.free_count()
+    for budget, steps in [(128, 5), (64, 3)]:
+        m = mass.cpu().numpy()
+        weights = [np.concatenate([m[i, :, :oracle.unpack_entry(int(e))[2]].T for i, e in
+                                   zip(range(batch.offsets_host[r], batch.offsets_host[r + 1]),
+                                       batch.entries.cpu().numpy().view(np.uint64)[batch.offsets_host[r]:])]) for r in range(R)]
+        batch, kept, mass = batch.evict(s.pool, mass, budget, sinks=4, recent=16, reserve=1)
+        for r in range(R):
+            for h in range(hkv):
+                ids = kept_tokens(weights[r][:, h], budget, 4, 16)
+                held[r][h] = (held[r][h][0][ids], held[r][h][1][ids])
+        wsd_n = L.lazyattn_workspace_size(s.pool.handle, L.LAZYATTN_OP_DECODE_MASS, batch.c)
+        wsd = torch.zeros(wsd_n, dtype=torch.uint8, device="cuda")
+        for t in range(steps):
+            q, kn, vn = step_inputs(s, R)
+            out = s.empty(R, s.hq, s.d)
+            old = mass.clone()
+            L.lazyattn_decode_mass(s.pool.handle, batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, mass, mass, 1.0, wsd, wsd_n)
+            got, add = out.float().cpu().numpy(), (mass - old).cpu().numpy()
+            for r in range(R):
+                for h in range(hkv):
+                    k, v = held[r][h]
+                    held[r][h] = np.r_[k, kn[r, h][None]], np.r_[v, vn[r, h][None]]
+                    k, v = held[r][h]
+                    g = s.hq // hkv
+                    want, w, reach = attend(s.spec, q[r, h * g:(h + 1) * g][None], k[:, None], v[:, None], [len(k) - 1],
+                                            np.arange(len(k)))
+                    compare(got[r, h * g:(h + 1) * g], want[0], "bf16")
+                    e0 = batch.offsets_host[r]
+                    seen = add[e0:batch.offsets_host[r + 1], h].reshape(-1)
+                    # the difference of two float32 totals below 256: half a step of each
+                    assert np.max(np.abs(seen[:len(k)] - w[:, 0])) <= 2.0 ** -16 + reach * 1e-5
+                    assert np.all(seen[len(k):] == 0)
+    wn = L.lazyattn_window_workspace_size(s.pool.handle, L.LAZYATTN_OP_DECODE, batch.c, 20, 4)
+    wsw = torch.zeros(wn, dtype=torch.uint8, device="cuda")
+    q, kn, vn = step_inputs(s, R)
+    out = s.empty(R, s.hq, s.d)
+    L.lazyattn_decode_window(s.pool.handle, batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, 20, 4, wsw, wn)
+    got = out.float().cpu().numpy()
+    for r in range(R):
+        k = np.stack([np.r_[held[r][h][0], kn[r, h][None]] for h in range(hkv)], 1)
+        v = np.stack([np.r_[held[r][h][1], vn[r, h][None]] for h in range(hkv)], 1)
+        want, _, _ = attend(s.spec, q[r][None], k, v, [len(k) - 1], np.arange(len(k)), 20, 4)
+        compare(got[r], want[0], "bf16")
+    assert s.pool.device_status() == 0
+    assert s.pool.free_count() < free0
+
+
+def test_captured_and_replayed(L):
+    """Every call in one CUDA graph on a side stream, replayed: the same bits as the eager calls."""
+    s = Scenario(L, [([300, 150], 64, 64), ([200, 77, 130], 40, 40)], seed=33, extra=64)
+    R = 2
+    q1, k1, v1 = (s.dev(x) for x in step_inputs(s, R))
+    q = s.dev(s.q)
+    per = 6
+    dst0 = torch.from_numpy(L.pack_entries(s.pool.alloc_pages(R * per), [0] * R * per, [0] * R * per, [1] * R * per)
+                            .view(np.int64).copy()).cuda()
+    off = torch.arange(R + 1, dtype=torch.int32, device="cuda") * per
+    entries0 = s.batch.entries.clone()
+    wsp = workspace(L, s, L.LAZYATTN_OP_PREFILL, 100, 4)
+    wsw = workspace(L, s, L.LAZYATTN_OP_DECODE, 100, 4)
+    wsm = workspace(L, s, L.LAZYATTN_OP_PREFILL_MASS)
+    wsd = workspace(L, s, L.LAZYATTN_OP_DECODE_MASS)
+    o = [s.empty(s.batch.total_q, s.hq, s.d), s.empty(R, s.hq, s.d), s.empty(R, s.hq, s.d)]
+    m = [torch.empty(s.n_entries(), s.hkv, 16, device="cuda") for _ in range(2)]
+    dst, kept, dm = dst0.clone(), torch.zeros(R, s.hkv, 80, dtype=torch.int32, device="cuda"), torch.empty(R * per, s.hkv, 16, device="cuda")
+
+    def calls():
+        h, c = s.pool.handle, s.batch.c
+        s.batch.entries.copy_(entries0)
+        L.lazyattn_prefill_window(h, c, q, o[0], 100, 4, *wsp)
+        L.lazyattn_prefill_mass(h, c, q, None, m[0], 1.0, *wsm)
+        L.lazyattn_decode_window(h, c, q1, k1, v1, o[1], 100, 4, *wsw)
+        L.lazyattn_decode_mass(h, c, q1, k1, v1, o[2], m[0], m[1], 0.5, *wsd)
+        L.lazyattn_evict(h, c, m[1], 80, 4, 16, dst, off, kept, dm)
+
+    results = o + m + [dst, kept, dm]
+    calls()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in results]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        calls()
+    for _ in range(3):
+        for x in results[:-3] + [kept, dm]:
+            x.zero_()
+        dst.copy_(dst0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(results, want):
+            assert torch.equal(a, b)
+    assert s.pool.device_status() == 0
