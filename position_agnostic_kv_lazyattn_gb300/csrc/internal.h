@@ -144,6 +144,17 @@ struct DecodeWs {
     size_t acc_off;       // float [R*Hkv*S][g][D]: unnormalised partial outputs
     size_t total;
     int splits;
+    // windowed decode: live entries per request, their lists, and (doc-local pools) their document offsets
+    size_t count_off = 0, list_off = 0, delta_off = 0;
+};
+
+// Live lists of a windowed decode step: request r's entries with a visible token,
+// in table order, at entries[r * cap ..].
+struct LiveLists {
+    int32_t* counts;      // [R]
+    uint64_t* entries;    // [R][cap]
+    int32_t* delta;       // [R][cap] doc-local pools, else NULL
+    int32_t cap, window, sinks;
 };
 
 // ---------------------------------------------------------------- decode plan
@@ -205,6 +216,9 @@ int launch_store_pages(const lazyattn_pool& p, const void* k, const void* v, int
                        const int32_t* pages_host, int32_t npages, cudaStream_t stream);
 int launch_decode_append(const lazyattn_pool& p, const lazyattn_batch& b, const void* k_new,
                          const void* v_new, int32_t* qpos, cudaStream_t stream);
+// The append, and the requests' live lists at the appended tokens' positions (bf16 pools).
+int launch_decode_append_list(const lazyattn_pool& p, const lazyattn_batch& b, const void* k_new, const void* v_new,
+                              int32_t* qpos, const LiveLists& lists, cudaStream_t stream);
 int launch_materialize(const lazyattn_pool& p, const lazyattn_batch& b, const uint64_t* dst,
                        cudaStream_t stream);
 int launch_resolve(const lazyattn_pool& p, const lazyattn_batch& b, const int32_t* out_offsets,
@@ -227,6 +241,12 @@ int decode_occupancy(int* ctas_per_sm);
 int launch_decode_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
                        __nv_bfloat16* out, void* ws, const DecodeWs& L, cudaStream_t stream);
 
+// bf16 windowed decode: append, live lists and attention.
+DecodeWs decode_window_ws_layout(const lazyattn_pool& p, const lazyattn_batch& b, int32_t window, int32_t sinks);
+int launch_decode_window_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
+                              const void* k_new, const void* v_new, __nv_bfloat16* out, int32_t window, int32_t sinks,
+                              void* ws, const DecodeWs& L, cudaStream_t stream);
+
 // bf16 decode through a plan: document-major units on tcgen05 / TMEM, then a
 // combine of each request's partial results.
 size_t decode_plan_ws_bytes(const lazyattn_pool& p, const lazyattn_plan& plan);
@@ -239,13 +259,15 @@ int launch_decode_shared(const lazyattn_pool& p, const lazyattn_batch& b, const 
 // pool creation, so that launches stay capturable in CUDA graphs).
 int prefill_init();
 // Split count of a bf16 prefill over the KV tiles (1: one CTA per request, KV
-// head and query pair) and the workspace bytes its partials take.
-int prefill_splits(const lazyattn_pool& p, const lazyattn_batch& b);
+// head and query pair) and the workspace bytes its partials take. A window of
+// INT32_MAX hides nothing.
+int prefill_splits(const lazyattn_pool& p, const lazyattn_batch& b, int32_t window, int32_t sinks);
 size_t prefill_ws_bytes(const lazyattn_pool& p, const lazyattn_batch& b, int splits);
 int launch_prefill_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
-                        __nv_bfloat16* out, void* ws, size_t ws_bytes, cudaStream_t stream);
+                        __nv_bfloat16* out, int32_t window, int32_t sinks, void* ws, size_t ws_bytes,
+                        cudaStream_t stream);
 
-// Windowed attention on CUDA cores (decode_qpos NULL: the batch's query rows).
+// Windowed attention of fp32 pools on CUDA cores (decode_qpos NULL: the batch's query rows).
 int launch_window_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void* q, void* out,
                        const int32_t* decode_qpos, int32_t window, int32_t sinks, cudaStream_t stream);
 

@@ -330,8 +330,7 @@ int launch_mass(const lazyattn_pool& p, const lazyattn_batch& b, const Params& P
 int launch_window_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void* q, void* out,
                        const int32_t* decode_qpos, int32_t window, int32_t sinks, cudaStream_t stream) {
     const Params P = make_params(p, b, decode_qpos, window, sinks, true);
-    return p.d.dtype == LAZYATTN_F32 ? launch_rows<float>(p, b, P, q, out, stream)
-                                     : launch_rows<__nv_bfloat16>(p, b, P, q, out, stream);
+    return launch_rows<float>(p, b, P, q, out, stream);
 }
 
 size_t mass_simt_ws_bytes(const lazyattn_pool& p, int64_t rows) {

@@ -24,7 +24,8 @@
 //     movmatrix).
 // Warps combine through shared memory; splits combine through a partial buffer
 // in the workspace, reduced by the last CTA of each (r, h) to arrive (atomic
-// ticket, nobody waits). Every wait on a TMA is bounded; on a timeout the warp
+// ticket, nobody waits). Under a window (WIN) the pages are those of the request's
+// live list, written by the append kernel: the table's entries with a visible token. Every wait on a TMA is bounded; on a timeout the warp
 // drains its copies and the CTA records LAZYATTN_EDEVICE.
 #include <limits.h>
 
@@ -62,6 +63,9 @@ struct DecodeParams {
     int splits;
     int g;
     const int32_t* entry_delta;   // doc-local pools: document offset of each entry
+    const int32_t* counts;        // WIN: live entries of each request; entries and entry_delta are then lists
+    int32_t list_cap;             // of list_cap places a request
+    int32_t window, sinks;
 };
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -173,7 +177,8 @@ __device__ __forceinline__ int slot_unit(int t, int f4) { return t * (kRowBytes 
 // (its position relative to the page's document), once per change of delta
 // (§3.2 "Decoding": rotate q per document rather than K per token).
 // ALIBI: no rotation of q or k; each score gets -slope_h (m - n) (§3.5).
-template <bool PREROT, bool LOCAL, bool ALIBI>
+// WIN: pages from the live lists; key n is visible iff n <= m and (m - n < window or n < sinks).
+template <bool PREROT, bool LOCAL, bool ALIBI, bool WIN>
 __global__ void __launch_bounds__(kThreads, 3)
     decode_bf16_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        PoolView pv, DecodeParams P) {
@@ -208,14 +213,18 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
     }
     __syncthreads();
-    const int e0 = P.entry_offsets[r], e1 = P.entry_offsets[r + 1];   // not written by the append
     int m = -1;   // logical position of the appended token: read from the append after grid_dep_wait()
 
-    const int chunk = (e1 - e0 + S - 1) / S;
-    const int cb = e0 + s * chunk;
-    const int ce = min(e1, cb + chunk);
-    const int n_w = ce - cb > warp ? (ce - cb - warp + kWarps - 1) / kWarps : 0;
-    const uint64_t* my_entries = P.entries + cb + warp;    // page i of this warp: my_entries[kWarps * i]
+    int cb = 0, n_w = 0;                      // this CTA's first entry; pages of this warp
+    const uint64_t* my_entries = P.entries;   // page i of this warp: my_entries[kWarps * i]
+    auto share = [&](int e0, int e1) {
+        const int chunk = (e1 - e0 + S - 1) / S;
+        cb = e0 + s * chunk;
+        const int ce = min(e1, cb + chunk);
+        n_w = ce - cb > warp ? (ce - cb - warp + kWarps - 1) / kWarps : 0;
+        my_entries = P.entries + (WIN ? (size_t)r * P.list_cap : 0) + cb + warp;
+    };
+    if (!WIN) share(P.entry_offsets[r], P.entry_offsets[r + 1]);   // not written by the append
     const uint32_t ring = smem_u32(sm + warp * kStages * kStageBytes);
     volatile int* abort_flag = &s_abort;
 
@@ -242,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     // page ahead (one float4 per lane, staged in the warp's row buffer when
     // the page comes up), so no global load latency sits inside the page loop.
     auto entry_at = [&](int i) { return i < n_w ? my_entries[kWarps * i] : 0ull; };
-    auto delta_at = [&](int i) { return (LOCAL && i < n_w) ? P.entry_delta[cb + warp + kWarps * i] : 0; };
+    auto delta_at = [&](int i) { return (LOCAL && i < n_w) ? P.entry_delta[(WIN ? (size_t)r * P.list_cap : 0) + cb + warp + kWarps * i] : 0; };
     // the page's row of the position table: its start (ROT_K) or m - delta (LOCAL)
     auto row_of = [&](uint64_t e, int d) {
         const int pos = LOCAL ? m - d : entry_start(e);
@@ -257,14 +266,15 @@ __global__ void __launch_bounds__(kThreads, 3)
     // but doc-local), the first pages of entries that are not writable are
     // requested before waiting for the append, and their loads overlap it.
     uint64_t e_cur = entry_at(0), e_n1 = entry_at(1);
-    const bool early0 = !LOCAL && !entry_writable(e_cur);
-    const bool early1 = !LOCAL && !entry_writable(e_n1);
+    const bool early0 = !LOCAL && !WIN && !entry_writable(e_cur);
+    const bool early1 = !LOCAL && !WIN && !entry_writable(e_n1);
     if (lane == 0) {
         if (early0) issue(0, e_cur, 0);
         if (early1) issue(1, e_n1, 0);
     }
     grid_dep_wait();
     m = P.qpos[r];
+    if (WIN) share(0, P.counts[r]);
     __nv_bfloat16* out_rh = P.out + ((size_t)r * Hq + (size_t)h * g) * kD;
     if (m < 0) {   // request without an appended token (status already recorded)
         if (lane == 0) {   // the early copies land before the CTA's shared memory is released
@@ -432,7 +442,12 @@ __global__ void __launch_bounds__(kThreads, 3)
             }
 
             // S^T fragment: (token gr | gr+8) x (head 2c | 2c+1)
-            const bool v0 = gr < nv, v1 = gr + 8 < nv;
+            bool v0 = gr < nv, v1 = gr + 8 < nv;
+            if (WIN) {   // a listed page has a visible token, so the maximum below is finite
+                const int n0 = entry_start(e) + gr, n1 = n0 + 8;
+                v0 = v0 && n0 <= m && (m - n0 < P.window || n0 < P.sinks);
+                v1 = v1 && n1 <= m && (m - n1 < P.window || n1 < P.sinks);
+            }
             if (ALIBI) {   // tokens start + gr, start + gr + 8; heads 2c, 2c + 1
                 const float dn = (float)(entry_start(e) + gr - m);
                 sacc[0] += al0 * dn;
@@ -620,11 +635,11 @@ __global__ void __launch_bounds__(kThreads, 3)
 //   cost(S) = ceil(CTAs / resident slots) * (kCtaOverhead + pages per warp).
 // Few long-lived CTAs win for small batches; large batches split until the
 // last wave is nearly full.
-int choose_splits(const lazyattn_pool& p, const lazyattn_batch& b) {
+int choose_splits(const lazyattn_pool& p, int num_requests, int max_pages) {
     constexpr double kCtaOverhead = 4.0;
-    const long W = (long)b.num_requests * p.d.n_kv_heads;
+    const long W = (long)num_requests * p.d.n_kv_heads;
     const long slots = std::max(p.decode_slots, 1);
-    const long pages = std::max(b.max_entries, 1);
+    const long pages = std::max(max_pages, 1);
     int best = 1;
     double best_cost = 1e300;
     for (int S = 1; S <= 32; ++S) {
@@ -644,27 +659,34 @@ inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
+using DecodeKernel = void (*)(const CUtensorMap, const CUtensorMap, PoolView, DecodeParams);
+
+template <bool WIN>
+static DecodeKernel decode_kernel_variant(bool prerot, bool local, bool alibi) {
+    if (alibi) return decode_bf16_kernel<false, false, true, WIN>;
+    if (local) return decode_bf16_kernel<false, true, false, WIN>;
+    return prerot ? decode_bf16_kernel<true, false, false, WIN> : decode_bf16_kernel<false, false, false, WIN>;
+}
+
 int decode_occupancy(int* ctas_per_sm) {
-    if (cudaFuncSetAttribute(decode_bf16_kernel<false, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(decode_bf16_kernel<true, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(decode_bf16_kernel<false, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(decode_bf16_kernel<false, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes) != cudaSuccess)
-        return LAZYATTN_ECUDA;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_bf16_kernel<false, false, false>, kThreads,
-                                                         kSmemBytes) == cudaSuccess
+    for (int i = 0; i < 8; ++i) {
+        const bool prerot = (i & 3) == 1, local = (i & 3) == 2, alibi = (i & 3) == 3;
+        DecodeKernel k = i < 4 ? decode_kernel_variant<false>(prerot, local, alibi)
+                               : decode_kernel_variant<true>(prerot, local, alibi);
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+            return LAZYATTN_ECUDA;
+    }
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_bf16_kernel<false, false, false, false>,
+                                                         kThreads, kSmemBytes) == cudaSuccess
                ? LAZYATTN_OK
                : LAZYATTN_ECUDA;
 }
 
-DecodeWs decode_ws_layout(const lazyattn_pool& p, const lazyattn_batch& b) {
+static DecodeWs ws_layout(const lazyattn_pool& p, const lazyattn_batch& b, int splits) {
     DecodeWs L;
     const size_t R = (size_t)b.num_requests, Hkv = (size_t)p.d.n_kv_heads;
     const size_t g = (size_t)(p.d.n_q_heads / p.d.n_kv_heads);
-    L.splits = choose_splits(p, b);
+    L.splits = splits;
     const size_t S = (size_t)L.splits;
     L.qpos_off = 0;
     L.ticket_off = up256(R * sizeof(int32_t));
@@ -674,11 +696,26 @@ DecodeWs decode_ws_layout(const lazyattn_pool& p, const lazyattn_batch& b) {
     return L;
 }
 
-int launch_decode_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
-                       __nv_bfloat16* out, void* ws, const DecodeWs& L, cudaStream_t stream) {
-    if (!p.have_maps) return LAZYATTN_ECUDA;
-    char* base = static_cast<char*>(ws);
-    DecodeParams P;
+DecodeWs decode_ws_layout(const lazyattn_pool& p, const lazyattn_batch& b) {
+    return ws_layout(p, b, choose_splits(p, b.num_requests, b.max_entries));
+}
+
+// A window of w positions and s sinks touches about w / 16 + s / 16 + 2 full pages
+// (tables of part-filled pages have more: their CTAs' runs get longer).
+DecodeWs decode_window_ws_layout(const lazyattn_pool& p, const lazyattn_batch& b, int32_t window, int32_t sinks) {
+    const int64_t pages = std::min<int64_t>(b.max_entries, (int64_t)window / kPage + (int64_t)sinks / kPage + 2);
+    DecodeWs L = ws_layout(p, b, choose_splits(p, b.num_requests, (int)pages));
+    const size_t places = (size_t)b.num_requests * (size_t)std::max(b.max_entries, 1);
+    L.count_off = L.total;
+    L.list_off = L.count_off + up256((size_t)b.num_requests * sizeof(int32_t));
+    L.delta_off = L.list_off + up256(places * sizeof(uint64_t));
+    L.total = L.delta_off + (p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL ? up256(places * sizeof(int32_t)) : 0);
+    return L;
+}
+
+static DecodeParams decode_params(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
+                                  __nv_bfloat16* out, char* base, const DecodeWs& L) {
+    DecodeParams P = {};
     P.entries = b.entries;
     P.entry_offsets = b.entry_offsets;
     P.q = q;
@@ -689,16 +726,50 @@ int launch_decode_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __
     P.acc = reinterpret_cast<float*>(base + L.acc_off);
     P.splits = L.splits;
     P.g = p.d.n_q_heads / p.d.n_kv_heads;
-    dim3 grid(L.splits, p.d.n_kv_heads, b.num_requests);
     P.entry_delta = b.entry_delta;
-    auto kern = p.d.position_encoding == LAZYATTN_POS_ALIBI ? decode_bf16_kernel<false, false, true>
-                : p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL
-                    ? decode_bf16_kernel<false, true, false>
-                    : ((b.flags & LAZYATTN_KEYS_PREROTATED) ? decode_bf16_kernel<true, false, false>
-                                                             : decode_bf16_kernel<false, false, false>);
+    return P;
+}
+
+static int launch(const lazyattn_pool& p, const lazyattn_batch& b, const DecodeParams& P, bool win, cudaStream_t stream) {
+    if (!p.have_maps) return LAZYATTN_ECUDA;
+    const bool prerot = (b.flags & LAZYATTN_KEYS_PREROTATED) != 0;
+    const bool local = p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL;
+    const bool alibi = p.d.position_encoding == LAZYATTN_POS_ALIBI;
+    DecodeKernel kern = win ? decode_kernel_variant<true>(prerot, local, alibi)
+                            : decode_kernel_variant<false>(prerot, local, alibi);
+    const dim3 grid(P.splits, p.d.n_kv_heads, b.num_requests);
     if (launch_dependent(kern, grid, dim3(kThreads), kSmemBytes, stream, p.kmap, p.vmap, p.view(), P) != cudaSuccess)
         return LAZYATTN_ECUDA;
     return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;
+}
+
+int launch_decode_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
+                       __nv_bfloat16* out, void* ws, const DecodeWs& L, cudaStream_t stream) {
+    return launch(p, b, decode_params(p, b, q, out, static_cast<char*>(ws), L), false, stream);
+}
+
+int launch_decode_window_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
+                              const void* k_new, const void* v_new, __nv_bfloat16* out, int32_t window, int32_t sinks,
+                              void* ws, const DecodeWs& L, cudaStream_t stream) {
+    char* base = static_cast<char*>(ws);
+    LiveLists lists;
+    lists.counts = reinterpret_cast<int32_t*>(base + L.count_off);
+    lists.entries = reinterpret_cast<uint64_t*>(base + L.list_off);
+    lists.delta = p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL ? reinterpret_cast<int32_t*>(base + L.delta_off) : nullptr;
+    lists.cap = std::max(b.max_entries, 1);
+    lists.window = window;
+    lists.sinks = sinks;
+    const int rc = launch_decode_append_list(p, b, k_new, v_new, reinterpret_cast<int32_t*>(base + L.qpos_off), lists,
+                                             stream);
+    if (rc != LAZYATTN_OK) return rc;
+    DecodeParams P = decode_params(p, b, q, out, base, L);
+    P.entries = lists.entries;
+    P.entry_delta = lists.delta;
+    P.counts = lists.counts;
+    P.list_cap = lists.cap;
+    P.window = window;
+    P.sinks = sinks;
+    return launch(p, b, P, true, stream);
 }
 
 }  // namespace lazyattn

@@ -152,23 +152,17 @@ __device__ int find_append_entry(const uint64_t* entries, int e0, int e1, int la
     return tail;
 }
 
-// One block per request: append k_new/v_new into the request's tail page.
-// Launched as a programmatic dependent of the previous kernel in the stream
-// (the previous step's attention): it lets its own dependent launch at once
-// and waits for the previous grid before touching the table or the pool.
+// Append k_new/v_new of request r into its tail page (called by a whole block).
 // MODE: 0 stores k as given (position-free keys); 1 rotates it at its logical
 // position (pre-rotated pages of the materialising baseline); 2 at its
 // document-local position, logical - entry_delta (doc-local pools).
 template <typename T, int MODE>
-__global__ void decode_append_kernel(PoolView pv, uint64_t* entries, const int32_t* entry_offsets,
-                                     const T* __restrict__ k_new, const T* __restrict__ v_new, int32_t* qpos,
-                                     const int32_t* entry_delta) {
+__device__ __forceinline__ void append_token(const PoolView& pv, uint64_t* entries, const int32_t* entry_offsets,
+                                             const T* __restrict__ k_new, const T* __restrict__ v_new, int32_t* qpos,
+                                             const int32_t* entry_delta, int r) {
     constexpr bool PREROT = MODE != 0;
-    const int r = blockIdx.x;
     __shared__ int s_entry;
     __shared__ uint64_t s_e;
-    grid_dep_launch_dependents();
-    grid_dep_wait();
     if (threadIdx.x < 32) {
         const int e0 = entry_offsets[r], e1 = entry_offsets[r + 1];
         int t = find_append_entry(entries, e0, e1, threadIdx.x);
@@ -282,6 +276,81 @@ __global__ void decode_append_kernel(PoolView pv, uint64_t* entries, const int32
         __threadfence();
         entries[s_entry] = make_entry(page, entry_start(e), slot + 1, true);
     }
+}
+
+// One block per request, launched as a programmatic dependent of the previous
+// kernel in the stream (the previous step's attention): it lets its own dependent
+// launch at once and waits for the previous grid before touching the table or the pool.
+template <typename T, int MODE>
+__global__ void decode_append_kernel(PoolView pv, uint64_t* entries, const int32_t* entry_offsets,
+                                     const T* __restrict__ k_new, const T* __restrict__ v_new, int32_t* qpos,
+                                     const int32_t* entry_delta) {
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    append_token<T, MODE>(pv, entries, entry_offsets, k_new, v_new, qpos, entry_delta, blockIdx.x);
+}
+
+// The append of a windowed step, then the request's live list: the entries with a
+// token at n <= m and (m - n < window or n < sinks), in table order. Each thread
+// takes kListRun consecutive entries, so a table of 4096 entries (65,536 tokens in full pages)
+// costs one round of loads and one scan. Unusable entries are reported and left out.
+constexpr int kListThreads = 256;
+constexpr int kListRun = 16;
+template <int MODE>
+__global__ void __launch_bounds__(kListThreads)
+    decode_append_list_kernel(PoolView pv, uint64_t* entries, const int32_t* entry_offsets,
+                              const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
+                              int32_t* qpos, const int32_t* entry_delta, LiveLists lists) {
+    __shared__ int s_sum[kListThreads / 32];
+    const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    append_token<__nv_bfloat16, MODE>(pv, entries, entry_offsets, k_new, v_new, qpos, entry_delta, r);
+    __syncthreads();   // the table entry and qpos written by thread 0
+    const int m = qpos[r];
+    const int e0 = entry_offsets[r], e1 = entry_offsets[r + 1];
+    int done = 0;
+    for (int base = e0; base < e1 && m >= 0; base += kListThreads * kListRun) {
+        uint64_t e[kListRun];
+        uint32_t live = 0;
+#pragma unroll
+        for (int j = 0; j < kListRun; ++j) {
+            const int i = base + threadIdx.x * kListRun + j;
+            e[j] = i < e1 ? entries[i] : 0ull;
+        }
+#pragma unroll
+        for (int j = 0; j < kListRun; ++j) {
+            const int n = entry_nvalid(e[j]), a = entry_start(e[j]), b = min(a + n - 1, m);
+            if (n > 0 && a <= m && (m - b < lists.window || a < lists.sinks) && entry_ok(pv, e[j])) live |= 1u << j;
+        }
+        int incl = __popc(live);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        __syncthreads();   // the sums of an earlier round have been read
+        if (lane == 31) s_sum[warp] = incl;
+        __syncthreads();
+        int at = done + incl - __popc(live);
+#pragma unroll
+        for (int w = 0; w < kListThreads / 32; ++w) {
+            if (w < warp) at += s_sum[w];
+            done += s_sum[w];
+        }
+#pragma unroll
+        for (int j = 0; j < kListRun; ++j) {
+            if (!((live >> j) & 1u)) continue;
+            if (at < lists.cap) {   // max_entries bounds a request's entries
+                lists.entries[(size_t)r * lists.cap + at] = e[j];
+                if (MODE == 2) lists.delta[(size_t)r * lists.cap + at] = entry_delta[base + threadIdx.x * kListRun + j];
+            } else {
+                record_error(pv.status, LAZYATTN_ERANGE);
+            }
+            ++at;
+        }
+    }
+    if (threadIdx.x == 0) lists.counts[r] = min(done, lists.cap);
 }
 
 // One block per (entry slot i of request r): copy the page into dst's page,
@@ -409,6 +478,18 @@ int launch_decode_append(const lazyattn_pool& p, const lazyattn_batch& b, const 
                              qpos, b.entry_delta) != cudaSuccess)
             return LAZYATTN_ECUDA;
     }
+    return cuda_status();
+}
+
+int launch_decode_append_list(const lazyattn_pool& p, const lazyattn_batch& b, const void* k_new, const void* v_new,
+                              int32_t* qpos, const LiveLists& lists, cudaStream_t stream) {
+    auto kern = p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL ? decode_append_list_kernel<2>
+                : (b.flags & LAZYATTN_KEYS_PREROTATED)     ? decode_append_list_kernel<1>
+                                                           : decode_append_list_kernel<0>;
+    if (launch_dependent(kern, dim3(b.num_requests), dim3(kListThreads), 0, stream, p.view(), b.entries, b.entry_offsets,
+                         static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new), qpos,
+                         b.entry_delta, lists) != cudaSuccess)
+        return LAZYATTN_ECUDA;
     return cuda_status();
 }
 

@@ -40,7 +40,11 @@
 // tcgen05.mma operations of one thread execute in issue order. The same order
 // means that when softmax i sees S_i of tile k, O_i already holds tile k-1.
 // Tiles whose keys are all masked for every row of the CTA (past the causal
-// edge, or empty entries) are skipped. Only the producer reads the block
+// edge, or empty entries) are skipped. Under a window (WIN) the whole CTA first
+// marks the live ones among the request's first kMarked tiles in a bit map, 512 tiles a
+// round, and the producer goes from mark to mark: walking every tile's entries on
+// one thread costs about 0.1 us a tile, which for a short window over a long
+// context is most of the kernel. Pages of a live tile without a visible key are not read. Only the producer reads the block
 // table. Every wait is bounded; a timeout raises an abort flag that all roles
 // honour, drains in-flight copies and MMAs, frees TMEM and records
 // LAZYATTN_EDEVICE.
@@ -62,6 +66,7 @@ constexpr int kRows = kTileM * kQTiles;
 constexpr int kN = 128;                            // keys per K/V tile
 constexpr int kPagesPerTile = kN / kPage;          // 8
 constexpr int kStages = 2;
+constexpr int kMarked = 8192;                      // WIN: tiles with a mark (1M tokens in full pages); later ones are all looked at
 constexpr int kInfoSlots = 4;                      // tile-info ring (power of two)
 constexpr int kThreads = 512;
 constexpr int kQBytes = kTileM * kD * 2;           // 32 KB
@@ -94,7 +99,8 @@ struct __align__(16) TileInfo {
     int n[kPagesPerTile];         // keys in each page (0: none / unusable)
     int y[kPagesPerTile];         // row of the page in the K/V tensor maps (out of range: zero fill)
     int full_from;                // every page full: rows at positions >= this see every key; else INT_MAX
-    int pad[3];
+    int full_to;                  // WIN: ... and at positions below this (a full tile's first key, plus the window)
+    int pad[2];
 };
 
 struct PrefillParams {
@@ -111,6 +117,7 @@ struct PrefillParams {
     int32_t row_blocks;           // rows of the position-table view (max_position / 16); 0: no view
     int32_t splits;               // CTAs per (request, KV head, query pair), each a share of the tiles
     int32_t qpairs;               // query pairs per request (grid.x / splits)
+    int32_t window, sinks;        // WIN
     float* part_o;                // splits > 1: [item][split][row][D] unnormalised O
     float2* part_ml;              // splits > 1: [item][split][row] (reference maximum, sum)
 };
@@ -207,7 +214,8 @@ __device__ __forceinline__ int usable_tokens(const PoolView& pv, uint64_t e) {
 // (§3.5, score-space positional methods), computed from logical positions.
 // SPLIT: the request's tiles are shared by P.splits CTAs, each writing partials
 // (a separate instantiation, so that the unsplit kernel's code is unchanged).
-template <bool PREROT, bool LOCAL, bool INTER, bool ALIBI, bool SPLIT>
+// WIN: key n is visible to row m iff n <= m and (m - n < P.window or n < P.sinks).
+template <bool PREROT, bool LOCAL, bool INTER, bool ALIBI, bool SPLIT, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ CUtensorMap kmap4, const __grid_constant__ CUtensorMap vmap4,
@@ -248,8 +256,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // This CTA's share of the request's tiles: [jb, jb + T)
     const int t_all = e1 > e0 ? (e1 - e0 + kPagesPerTile - 1) / kPagesPerTile : 0;
     const int chunk = SPLIT ? (t_all + P.splits - 1) / P.splits : t_all;
-    const int jb = SPLIT ? min(t_all, split * chunk) : 0;
-    const int T = SPLIT ? min(t_all, jb + chunk) - jb : t_all;
+    const int jb = SPLIT && !WIN ? min(t_all, split * chunk) : 0;
+    const int T = SPLIT && !WIN ? min(t_all, jb + chunk) - jb : t_all;
+    // WIN: a page is live iff one of its tokens is visible to some row of the CTA
+    const int m_lo = qs + i0;
+    auto page_live = [&](uint64_t e) {
+        const int n = entry_nvalid(e), a = entry_start(e);
+        return n > 0 && a <= m_hi && (!WIN || m_lo - (a + n - 1) < P.window || a < P.sinks);
+    };
 
     if (threadIdx.x == 0) {
         s_abort = 0;
@@ -273,6 +287,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
         tmem_alloc(smem_u32(&s_tmem), kTmemCols);
         tmem_relinquish();
+    }
+    __shared__ uint32_t s_live[WIN ? kMarked / 32 : 1];
+    if (WIN) {
+        for (int j0 = 0; j0 < min(T, kMarked); j0 += kThreads) {
+            const int j = j0 + (int)threadIdx.x;
+            bool live = false;
+            uint64_t e[kPagesPerTile];
+#pragma unroll
+            for (int p = 0; p < kPagesPerTile; ++p) {
+                const int idx = e0 + j * kPagesPerTile + p;
+                e[p] = j < T && idx < e1 ? P.entries[idx] : 0ull;
+            }
+#pragma unroll
+            for (int p = 0; p < kPagesPerTile; ++p) live = live || page_live(e[p]);
+            const unsigned bits = __ballot_sync(0xffffffffu, live);
+            if (lane == 0) s_live[j >> 5] = bits;
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -307,11 +338,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < kStages; ++s) last_k[s] = -1;
             uint64_t cur[kPagesPerTile], nxt[kPagesPerTile] = {};
             int curd[kPagesPerTile] = {}, nxtd[kPagesPerTile] = {};   // LOCAL: document offsets
-            load_entries(0, cur, curd);
+            // the first tile at or after j to look at, T if none
+            auto candidate = [&](int j) {
+                if (!WIN) return j;
+                const int marked = min(T, kMarked);
+                for (int w = j >> 5; j < marked; ++w) {
+                    const uint32_t bits = s_live[w] & (~0u << (j & 31));
+                    if (bits) return w * 32 + __ffs(bits) - 1;
+                    j = (w + 1) * 32;
+                }
+                return min(j, T);
+            };
+            int first = candidate(0), share = INT_MAX;   // WIN: this CTA's first tile, and how many it takes
+            if (SPLIT && WIN) {
+                int total = 0;
+                for (int j = first; j < T; j = candidate(j + 1)) ++total;
+                share = (total + P.splits - 1) / P.splits;
+                for (int i = split * share; i > 0 && first < T; --i) first = candidate(first + 1);
+            }
+            if (first < T) load_entries(first, cur, curd);
             int k = 0;
             bool ok = true;
-            for (int j = 0; j <= T; ++j) {
-                if (j + 1 < T) load_entries(j + 1, nxt, nxtd);
+            for (int j = first, taken = 0, next = 0; j <= T; j = next, ++taken) {
+                if (SPLIT && WIN && taken >= share) j = T;
+                next = j < T ? candidate(j + 1) : T + 1;
+                if (next < T) load_entries(next, nxt, nxtd);
                 int n[kPagesPerTile];
                 bool live = false;
 #pragma unroll
@@ -320,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (LOCAL && n[p] > 0 &&
                         (curd[p] < 0 || curd[p] > entry_start(cur[p]) || curd[p] >= pv.max_position))
                         n[p] = -1;
+                    if (WIN && !page_live(cur[p])) n[p] = min(n[p], 0);
                     live = live || (n[p] > 0 && entry_start(cur[p]) <= m_hi);
                 }
                 if (j == T || live) {
@@ -407,7 +459,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int p = 0; p < kPagesPerTile; ++p)
                         full_from = nn[p] == kPage ? max(full_from, ss[p] + kPage - 1) : INT_MAX;
-                    iv[7] = make_int4(full_from, 0, 0, 0);
+                    int full_to = INT_MAX;
+                    if (WIN) {
+                        int lo = INT_MAX, hi = 0;
+#pragma unroll
+                        for (int p = 0; p < kPagesPerTile; ++p) {
+                            lo = min(lo, ss[p]);
+                            hi = max(hi, ss[p] + kPage);
+                        }
+                        if (hi > P.sinks) full_to = lo <= INT_MAX - P.window ? lo + P.window : INT_MAX;
+                    }
+                    iv[7] = make_int4(full_from, full_to, 0, 0);
                     mbar_arrive(ib);   // releases the info writes to the other roles
                     mbar_arrive(fb);
                     if (bad) record_error(pv.status, LAZYATTN_ERANGE);
@@ -756,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const TileInfo& info = s_info[is];
             if (info.j < 0) break;
             // a warp whose rows all see every key of the tile skips the masking
-            const bool wfull = __all_sync(0xffffffffu, row_valid && m_row >= info.full_from);
+            const bool wfull = __all_sync(0xffffffffu, row_valid && m_row >= info.full_from && (!WIN || m_row < info.full_to));
             // visibility of the tile's keys to this row: bit i of visN is key
             // 32N + i (pages 2N and 2N+1 hold slots [0, lim) of their 16)
             uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
@@ -767,7 +829,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int hp = 0; hp < 2; ++hp) {
                     const int p = 2 * w + hp;
                     const int l = row_valid ? max(min(info.n[p], m_row - info.start[p] + 1), 0) : 0;
-                    bits |= ((1u << l) - 1u) << (16 * hp);
+                    uint32_t seen = (1u << l) - 1u;
+                    if (WIN) {   // slots [a, b) are past the sinks and before the window
+                        const int a = min(max(P.sinks - info.start[p], 0), kPage);
+                        const int b = min(max(m_row - P.window + 1 - info.start[p], 0), kPage);
+                        if (a < b) seen &= ~(((1u << b) - 1u) & ~((1u << a) - 1u));
+                    }
+                    bits |= seen << (16 * hp);
                 }
                 vis[w] = bits;
             }
@@ -995,27 +1063,33 @@ using PrefillKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUten
 
 // The instantiation for a pool and a batch: key layout and pairing of the pool,
 // pre-rotated pages of the batch.
-template <bool SPLIT>
+template <bool SPLIT, bool WIN>
 PrefillKernel prefill_kernel_variant(bool prerot, bool local, bool inter, bool alibi) {
-    if (alibi) return prefill_tc_kernel<false, false, false, true, SPLIT>;
+    if (alibi) return prefill_tc_kernel<false, false, false, true, SPLIT, WIN>;
     if (local)
-        return inter ? prefill_tc_kernel<false, true, true, false, SPLIT> : prefill_tc_kernel<false, true, false, false, SPLIT>;
+        return inter ? prefill_tc_kernel<false, true, true, false, SPLIT, WIN>
+                     : prefill_tc_kernel<false, true, false, false, SPLIT, WIN>;
     if (prerot)
-        return inter ? prefill_tc_kernel<true, false, true, false, SPLIT> : prefill_tc_kernel<true, false, false, false, SPLIT>;
-    return inter ? prefill_tc_kernel<false, false, true, false, SPLIT> : prefill_tc_kernel<false, false, false, false, SPLIT>;
+        return inter ? prefill_tc_kernel<true, false, true, false, SPLIT, WIN>
+                     : prefill_tc_kernel<true, false, false, false, SPLIT, WIN>;
+    return inter ? prefill_tc_kernel<false, false, true, false, SPLIT, WIN>
+                 : prefill_tc_kernel<false, false, false, false, SPLIT, WIN>;
 }
 
-PrefillKernel prefill_kernel_for(bool prerot, bool local, bool inter, bool alibi, bool split) {
-    return split ? prefill_kernel_variant<true>(prerot, local, inter, alibi)
-                 : prefill_kernel_variant<false>(prerot, local, inter, alibi);
+PrefillKernel prefill_kernel_for(bool prerot, bool local, bool inter, bool alibi, bool split, bool win) {
+    if (win)
+        return split ? prefill_kernel_variant<true, true>(prerot, local, inter, alibi)
+                     : prefill_kernel_variant<false, true>(prerot, local, inter, alibi);
+    return split ? prefill_kernel_variant<true, false>(prerot, local, inter, alibi)
+                 : prefill_kernel_variant<false, false>(prerot, local, inter, alibi);
 }
 
 int prefill_init() {
-    for (int sp = 0; sp < 2; ++sp)
+    for (int sw = 0; sw < 4; ++sw)
         for (int i = 0; i < 9; ++i) {
             if (i < 8 && (i & 1) && (i & 2)) continue;   // pre-rotated pages are never doc-local
-            PrefillKernel k = i == 8 ? prefill_kernel_for(false, false, false, true, sp)
-                                     : prefill_kernel_for(i & 1, i & 2, i & 4, false, sp);
+            PrefillKernel k = i == 8 ? prefill_kernel_for(false, false, false, true, sw & 1, sw & 2)
+                                     : prefill_kernel_for(i & 1, i & 2, i & 4, false, sw & 1, sw & 2);
             if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
                 return LAZYATTN_ECUDA;
         }
@@ -1030,12 +1104,15 @@ int prefill_init() {
 // read: about 6 MB per tile's time, merge launch included). Both constants are
 // fitted to GB300 timings of the TTFT-sweep batches at s = 1..4. The model picks
 // the s in 1..4 with the least estimated time; shares stay at least 8 tiles.
-int prefill_splits(const lazyattn_pool& p, const lazyattn_batch& b) {
+// Under a window a CTA's tiles are those of the window before its query tokens, of
+// the tokens themselves and of the sinks.
+int prefill_splits(const lazyattn_pool& p, const lazyattn_batch& b, int32_t window, int32_t sinks) {
     const int g = p.d.n_q_heads / p.d.n_kv_heads;
     if (p.d.dtype != LAZYATTN_BF16 || p.d.head_dim != kD || kRows % g != 0 || b.max_q_len < 1) return 1;
     const int64_t TQ = kRows / g;
     const int64_t items = (int64_t)b.num_requests * p.d.n_kv_heads * ((b.max_q_len + TQ - 1) / TQ);
-    const int64_t T = ((int64_t)b.max_entries + kPagesPerTile - 1) / kPagesPerTile;
+    const int64_t seen = ((int64_t)window + TQ + kN - 1) / kN + ((int64_t)sinks + kN - 1) / kN + 1;
+    const int64_t T = std::min(((int64_t)b.max_entries + kPagesPerTile - 1) / kPagesPerTile, seen);
     const int64_t sms = p.sm_count > 0 ? p.sm_count : 1;
     const double merge_bytes_per_tile = 6e6, startup_tiles = 5.0;
     int best = 1;
@@ -1064,7 +1141,9 @@ size_t prefill_ws_bytes(const lazyattn_pool& p, const lazyattn_batch& b, int spl
 }
 
 int launch_prefill_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
-                        __nv_bfloat16* out, void* ws, size_t ws_bytes, cudaStream_t stream) {
+                        __nv_bfloat16* out, int32_t window, int32_t sinks, void* ws, size_t ws_bytes,
+                        cudaStream_t stream) {
+    const bool win = window < p.d.max_position;   // else it hides nothing
     const int g = p.d.n_q_heads / p.d.n_kv_heads;
     if (p.d.head_dim != kD || kRows % g != 0) return LAZYATTN_EINVAL;
     if (!p.have_maps) return LAZYATTN_ECUDA;
@@ -1084,7 +1163,9 @@ int launch_prefill_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const _
     P.row_blocks = p.have_rmap ? p.d.max_position / kPage : 0;
     const int TQ = kRows / g;
     P.qpairs = (b.max_q_len + TQ - 1) / TQ;
-    P.splits = prefill_splits(p, b);
+    P.splits = prefill_splits(p, b, window, sinks);
+    P.window = window;
+    P.sinks = sinks;
     P.part_o = nullptr;
     P.part_ml = nullptr;
     if (P.splits > 1) {
@@ -1101,7 +1182,7 @@ int launch_prefill_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const _
     dim3 grid(P.qpairs * P.splits, p.d.n_kv_heads, b.num_requests);
     auto kern = prefill_kernel_for((b.flags & LAZYATTN_KEYS_PREROTATED) != 0,
                                    p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL, p.d.rope_interleaved != 0,
-                                   p.d.position_encoding == LAZYATTN_POS_ALIBI, P.splits > 1);
+                                   p.d.position_encoding == LAZYATTN_POS_ALIBI, P.splits > 1, win);
     kern<<<grid, kThreads, kSmemBytes, stream>>>(p.kmap, p.vmap, p.kmap4, p.vmap4, p.kmap8, p.vmap8, p.rmap, p.view(),
                                                  P);
     if (cudaGetLastError() != cudaSuccess) return LAZYATTN_ECUDA;

@@ -356,11 +356,15 @@ static size_t qpos_bytes(const lazyattn_batch* b) {
     return ((size_t)b->num_requests * sizeof(int32_t) + 255) & ~size_t(255);
 }
 
+static size_t prefill_bytes(const lazyattn_pool* pool, const lazyattn_batch* b, int32_t window, int32_t sinks) {
+    const int splits = pool->d.dtype == LAZYATTN_BF16 ? prefill_splits(*pool, *b, window, sinks) : 1;
+    return splits > 1 ? prefill_ws_bytes(*pool, *b, splits) : 256;
+}
+
 size_t lazyattn_workspace_size(lazyattn_pool_t pool, int32_t op, const lazyattn_batch* batch) {
     if (check_batch(pool, batch, op) != LAZYATTN_OK) return 0;
     if (op == LAZYATTN_OP_PREFILL) {
-        const int splits = pool->d.dtype == LAZYATTN_BF16 ? prefill_splits(*pool, *batch) : 1;
-        return splits > 1 ? prefill_ws_bytes(*pool, *batch, splits) : 256;
+        return prefill_bytes(pool, batch, INT32_MAX, 0);
     }
     if (op == LAZYATTN_OP_PREFILL_MASS) return mass_simt_ws_bytes(*pool, batch->total_q) + 256;
     if (op == LAZYATTN_OP_DECODE_MASS) return qpos_bytes(batch) + mass_simt_ws_bytes(*pool, batch->num_requests);
@@ -383,7 +387,7 @@ int lazyattn_prefill(lazyattn_pool_t pool, const lazyattn_batch* batch, const vo
         return launch_attention_f32(*pool, *batch, static_cast<const float*>(q), static_cast<float*>(out),
                                     nullptr, st);
     return launch_prefill_bf16(*pool, *batch, static_cast<const __nv_bfloat16*>(q),
-                               static_cast<__nv_bfloat16*>(out), workspace, workspace_bytes, st);
+                               static_cast<__nv_bfloat16*>(out), INT32_MAX, 0, workspace, workspace_bytes, st);
 }
 
 int lazyattn_decode(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const void* k_new,
@@ -426,9 +430,8 @@ size_t lazyattn_window_workspace_size(lazyattn_pool_t pool, int32_t op, const la
     if ((op != LAZYATTN_OP_PREFILL && op != LAZYATTN_OP_DECODE) || check_no_plan(pool, batch, op) != LAZYATTN_OK ||
         !window_ok(window, sinks))
         return 0;
-    if (op == LAZYATTN_OP_PREFILL)
-        return window >= pool->d.max_position ? lazyattn_workspace_size(pool, op, batch) : 256;
-    return qpos_bytes(batch);
+    if (op == LAZYATTN_OP_PREFILL) return prefill_bytes(pool, batch, window, sinks);
+    return pool->d.dtype == LAZYATTN_F32 ? qpos_bytes(batch) : decode_window_ws_layout(*pool, *batch, window, sinks).total;
 }
 
 int lazyattn_prefill_window(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, void* out, int32_t window,
@@ -440,9 +443,11 @@ int lazyattn_prefill_window(lazyattn_pool_t pool, const lazyattn_batch* batch, c
     if (!q || !out || !aligned16(q) || !aligned16(out)) return LAZYATTN_EINVAL;
     rc = check_device(pool);
     if (rc != LAZYATTN_OK) return rc;
-    // A window of every position hides nothing: the same call as without one.
-    if (window >= pool->d.max_position) return lazyattn_prefill(pool, batch, q, out, workspace, workspace_bytes, stream);
-    return launch_window_simt(*pool, *batch, q, out, nullptr, window, sinks, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pool->d.dtype == LAZYATTN_F32) return launch_window_simt(*pool, *batch, q, out, nullptr, window, sinks, st);
+    // (a window of every position hides nothing: the same kernel as without one)
+    return launch_prefill_bf16(*pool, *batch, static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(out),
+                               window, sinks, workspace, workspace_bytes, st);
 }
 
 int lazyattn_decode_window(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const void* k_new,
@@ -458,6 +463,10 @@ int lazyattn_decode_window(lazyattn_pool_t pool, const lazyattn_batch* batch, co
     rc = check_device(pool);
     if (rc != LAZYATTN_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pool->d.dtype == LAZYATTN_BF16)
+        return launch_decode_window_bf16(*pool, *batch, static_cast<const __nv_bfloat16*>(q), k_new, v_new,
+                                         static_cast<__nv_bfloat16*>(out), window, sinks, workspace,
+                                         decode_window_ws_layout(*pool, *batch, window, sinks), st);
     int32_t* qpos = static_cast<int32_t*>(workspace);
     rc = launch_decode_append(*pool, *batch, k_new, v_new, qpos, st);
     if (rc != LAZYATTN_OK) return rc;

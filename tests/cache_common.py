@@ -1,5 +1,7 @@
 """Scenarios and the 64-bit reference of the operators that keep a cache small:
 windowed attention, attention mass, eviction."""
+import dataclasses
+
 import numpy as np
 import torch
 
@@ -30,6 +32,7 @@ class Scenario:
 
     def __init__(self, L, requests, mode="rope", dtype="bf16", hq=8, hkv=2, d=128, spare=1, seed=0, q_scale=2.0, extra=0,
                  gap=0):
+        self.rounded = mode in ("prerotated", "doc_local")   # keys stored rotated, in bf16
         self.L, self.mode, self.dtype, self.hq, self.hkv, self.d = L, mode, dtype, hq, hkv, d
         self.spec = spec_of(mode)
         rng = np.random.default_rng(seed)
@@ -98,8 +101,16 @@ class Scenario:
         return out
 
 
+@dataclasses.dataclass
+class Reference:
+    out: np.ndarray      # [rows][Hq][D]
+    spread: np.ndarray   # sum of p |v|, like out
+    mass: np.ndarray     # [n][Hkv]
+    reach: float         # largest sum |q_i k_i| of a score (ALiBi: or bias), in the log2 domain
+
+
 def attend(spec, q, k, v, q_pos, k_pos, window=None, sinks=0, causal=True):
-    """(out [rows][Hq][D], mass [n][Hkv], largest sum |q_i k_i| of a score in the log2 domain), in 64 bits."""
+    """Attention of the rows and the weight each key gets, in 64 bits."""
     q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
     q_pos, k_pos = np.asarray(q_pos, np.int64), np.asarray(k_pos, np.int64)
     rows, hq, d = q.shape
@@ -113,31 +124,49 @@ def attend(spec, q, k, v, q_pos, k_pos, window=None, sinks=0, causal=True):
     see = n <= m if causal else np.ones((rows, len(k_pos)), bool)
     if window is not None:
         see = see & ((m - n < window) | (n < sinks))
-    out, mass, reach = np.zeros((rows, hq, d)), np.zeros((len(k_pos), hkv)), 0.0
+    ref = Reference(np.zeros((rows, hq, d)), np.zeros((rows, hq, d)), np.zeros((len(k_pos), hkv)), 0.0)
     for h in range(hq):
         s = q[:, h] @ k[:, h // g].T * scale
-        reach = max(reach, float((np.abs(q[:, h]) @ np.abs(k[:, h // g]).T).max(initial=0.0) * scale * 1.4427))
+        ref.reach = max(ref.reach, float((np.abs(q[:, h]) @ np.abs(k[:, h // g]).T).max(initial=0.0) * scale * 1.4427))
         if slopes is not None:
             s = s - slopes[h] * (m - n)
-            reach = max(reach, float((slopes[h] * np.abs(m - n)).max(initial=0.0)) * 1.4427)
+            ref.reach = max(ref.reach, float((slopes[h] * np.abs(m - n)).max(initial=0.0)) * 1.4427)
         s = np.where(see, s, -np.inf)
         top = s.max(1, keepdims=True, initial=-np.inf)
         p = np.where(see, np.exp(s - np.where(np.isfinite(top), top, 0.0)), 0.0)
         total = p.sum(1, keepdims=True)
         p = np.divide(p, total, out=np.zeros_like(p), where=total > 0)
-        out[:, h] = p @ v[:, h // g]
-        mass[:, h // g] += p.sum(0)
-    return out, mass, reach
+        ref.out[:, h], ref.spread[:, h] = p @ v[:, h // g], p @ np.abs(v[:, h // g])
+        ref.mass[:, h // g] += p.sum(0)
+    return ref
+
+
+def check_out(got, ref, dtype, rounded=False, row=slice(None)):
+    """fp32 pools: max-abs 1e-4, as everywhere. bf16 pools, per element: the weights are rounded to bf16 for the product
+    with V (half a step, 2^-8, of sum p |v|) and the output once more (2^-8 of it); a score's error is at most the fp16
+    roundings of the rotated q and k (2^-11 each) of `reach`, and a weight and its row's sum each carry it, times ln 2.
+    Keys stored rotated (`rounded`) were rounded to bf16 before (2^-8). In the norm these average out: 5e-3, as everywhere."""
+    got, want, spread = np.asarray(got, np.float64), ref.out[row], ref.spread[row]
+    assert got.shape == want.shape and np.all(np.isfinite(got))
+    err = np.abs(got - want)
+    if dtype == "f32":
+        assert err.max(initial=0.0) <= 1e-4, err.max()
+        return
+    rel = 2.0 ** -8 + 2 * np.log(2) * ref.reach * (2.0 ** -10 + (2.0 ** -8 if rounded else 0.0))
+    worst = np.max(err - rel * spread - 2.0 ** -8 * np.abs(want))
+    assert worst <= 0, worst
+    norm = np.linalg.norm(err) / max(np.linalg.norm(want), 1e-300)
+    assert norm <= 5e-3, norm
 
 
 def check_mass(got, want, reach, rounded=False):
-    """A score's error (log2 units) is at most 63 steps of 2^-24 of the sum of its terms' sizes (`reach`): six roundings in
-    the rotation of each operand, three in the split into two fp16 numbers and the dropped product, and up to 24
-    accumulations that may truncate (two half steps each). The weight and its row's sum each carry that error, times ln 2;
+    """A score's error (log2 units) is at most 72 steps of 2^-24 of the sum of its terms' sizes (`reach`): six roundings in
+    the rotation of each operand, 12 in the split into two fp16 numbers (2^-22 each and for the dropped product) and 24
+    accumulations that may truncate (2^-23 each). The weight and its row's sum each carry that error, times ln 2;
     2^-19 for the exponentials and the sums. Keys stored rotated (`rounded`: materialised or document-local pages) were
-    rounded to bf16: half a step, 2^-9, per element."""
+    rounded to bf16: half a step, 2^-8, per element."""
     got, want = np.asarray(got, np.float64), np.asarray(want, np.float64)
     assert got.shape == want.shape and np.all(np.isfinite(got))
-    rel = 2 * np.log(2) * reach * (63 * 2.0 ** -24 + (2.0 ** -9 if rounded else 0.0)) + 2.0 ** -19
+    rel = 2 * np.log(2) * reach * (72 * 2.0 ** -24 + (2.0 ** -8 if rounded else 0.0)) + 2.0 ** -19
     worst = np.max(np.abs(got - want) - rel * want)
     assert worst <= 1e-30, (worst, rel)

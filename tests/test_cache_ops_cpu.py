@@ -51,16 +51,16 @@ def test_the_reference_without_a_window_is_the_oracle():
     q, k, v = rng.standard_normal((5, 4, 64)), rng.standard_normal((37, 2, 64)), rng.standard_normal((37, 2, 64))
     q_pos, k_pos = np.arange(32, 37), np.arange(37)
     for spec in (1e4, oracle.AlibiSpec()):
-        out, mass, _ = attend(spec, q, k, v, q_pos, k_pos)
-        np.testing.assert_allclose(out, oracle.attention(q, k, v, q_pos, k_pos, spec), atol=1e-12)
-        np.testing.assert_allclose(mass.sum(), 5 * 4, rtol=1e-12)
+        ref = attend(spec, q, k, v, q_pos, k_pos)
+        np.testing.assert_allclose(ref.out, oracle.attention(q, k, v, q_pos, k_pos, spec), atol=1e-12)
+        np.testing.assert_allclose(ref.mass.sum(), 5 * 4, rtol=1e-12)
 
 
 def test_the_reference_with_a_window_is_the_oracle_on_the_visible_tokens():
     rng = np.random.default_rng(1)
     q, k, v = rng.standard_normal((3, 4, 64)), rng.standard_normal((37, 2, 64)), rng.standard_normal((37, 2, 64))
     for window, sinks in [(1, 0), (5, 2), (100, 0), (4, 40)]:
-        out, _, _ = attend(1e4, q, k, v, np.arange(34, 37), np.arange(37), window, sinks)
+        ref = attend(1e4, q, k, v, np.arange(34, 37), np.arange(37), window, sinks)
         for i, m in enumerate(range(34, 37)):
             see = np.array([n for n in range(m + 1) if m - n < window or n < sinks])
-            np.testing.assert_allclose(out[i], oracle.attention(q[i:i + 1], k[see], v[see], [m], see, 1e4)[0], atol=1e-12)
+            np.testing.assert_allclose(ref.out[i], oracle.attention(q[i:i + 1], k[see], v[see], [m], see, 1e4)[0], atol=1e-12)

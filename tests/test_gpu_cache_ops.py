@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle
-from tests.cache_common import MODES, Scenario, attend, check_mass
+from tests.cache_common import MODES, Scenario, attend, check_mass, check_out
 from tests.gpu_common import compare
 
 pytestmark = pytest.mark.gpu
@@ -41,8 +41,8 @@ def check_prefill_window(L, s, window, sinks):
     for r, rows in enumerate(s.rows):
         if not rows:
             continue
-        want, _, _ = attend(s.spec, s.q[s.row_slice(r)], s.k[r], s.v[r], s.starts[r] + np.arange(rows), s.pos[r], window, sinks)
-        compare(got[s.row_slice(r)], want, s.dtype)
+        want = attend(s.spec, s.q[s.row_slice(r)], s.k[r], s.v[r], s.starts[r] + np.arange(rows), s.pos[r], window, sinks)
+        check_out(got[s.row_slice(r)], want, s.dtype, s.rounded)
     assert s.pool.device_status() == 0
 
 
@@ -96,11 +96,11 @@ def test_prefill_window_rows_that_see_nothing(L):
     c = L.lazyattn.make_batch(1, b.max_entries, b2.entries, b.entry_offsets, off, qs, 64, 64)
     out = s.empty(64, s.hq, s.d)
     L.lazyattn_prefill_window(s.pool.handle, c, s.dev(q), out, 30, 0)
-    want, _, _ = attend(s.spec, q, s.k[0], s.v[0], start + np.arange(64), s.pos[0], 30, 0)
-    assert np.all(want[:60] == 0) and np.any(want[60:] != 0)
+    want = attend(s.spec, q, s.k[0], s.v[0], start + np.arange(64), s.pos[0], 30, 0)
+    assert np.all(want.out[:60] == 0) and np.any(want.out[60:] != 0)
     got = out.float().cpu().numpy()
     assert np.all(got[:60] == 0)
-    compare(got, want, "bf16")
+    check_out(got, want, "bf16")
 
 
 def decode_state(s):
@@ -129,8 +129,8 @@ def check_decode_window(L, s, window, sinks, steps):
         for r in range(R):
             m = int(pos[r][-1]) + 1 if len(pos[r]) else 0
             k[r], v[r], pos[r] = np.r_[k[r], kn[r][None]], np.r_[v[r], vn[r][None]], np.r_[pos[r], m]
-            want, _, _ = attend(s.spec, q[r][None], k[r], v[r], [m], pos[r], window, sinks)
-            compare(got[r], want[0], s.dtype)
+            want = attend(s.spec, q[r][None], k[r], v[r], [m], pos[r], window, sinks)
+            check_out(got[r], want, s.dtype, s.rounded, 0)
             if window == 1 and sinks == 0:   # its own value, bit for bit
                 np.testing.assert_array_equal(got[r], np.repeat(vn[r], s.hq // s.hkv, 0))
     assert s.pool.device_status() == 0
@@ -175,8 +175,8 @@ def test_decode_window_without_a_slot(L):
     L.lazyattn_decode_window(s.pool.handle, s.batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, 30, 2, ws, n)
     got = out.float().cpu().numpy()
     assert np.all(got[0] == 0)
-    want, _, _ = attend(s.spec, q[1][None], np.r_[s.k[1], kn[1][None]], np.r_[s.v[1], vn[1][None]], [25], np.arange(26), 30, 2)
-    compare(got[1], want[0], "bf16")
+    want = attend(s.spec, q[1][None], np.r_[s.k[1], kn[1][None]], np.r_[s.v[1], vn[1][None]], [25], np.arange(26), 30, 2)
+    check_out(got[1], want, "bf16", row=0)
     assert s.pool.device_status() == L.LAZYATTN_ENODECODE
 
 
@@ -193,10 +193,10 @@ def check_prefill_mass(L, s, decay, old):
     assert bool(torch.isnan(out[-1]).all())                                    # behind the table: left alone
     want, reach = [], 0.0
     for r, rows in enumerate(s.rows):
-        _, w, top = attend(s.spec, s.q[s.row_slice(r)], s.k[r], s.v[r], s.starts[r] + np.arange(rows), s.pos[r])
-        want.append(w + (np.float32(decay) * before[r].astype(np.float64) if old else 0.0))
-        reach = max(reach, top)
-    check_mass(out[:-1].cpu().numpy(), s.mass_of(want), reach, s.mode in ("prerotated", "doc_local"))
+        ref = attend(s.spec, s.q[s.row_slice(r)], s.k[r], s.v[r], s.starts[r] + np.arange(rows), s.pos[r])
+        want.append(ref.mass + (np.float32(decay) * before[r].astype(np.float64) if old else 0.0))
+        reach = max(reach, ref.reach)
+    check_mass(out[:-1].cpu().numpy(), s.mass_of(want), reach, s.rounded)
     again = torch.full_like(out, float("nan"))
     L.lazyattn_prefill_mass(s.pool.handle, s.batch.c, q, mass_in, again, decay, ws, n)
     assert torch.equal(out[:-1], again[:-1])                                   # equal calls, equal bits
@@ -256,11 +256,11 @@ def check_decode_mass(L, s, decay, steps, spare_mass=True):
         for r in range(R):
             m = int(pos[r][-1]) + 1 if len(pos[r]) else 0
             k[r], v[r], pos[r] = np.r_[k[r], kn[r][None]], np.r_[v[r], vn[r][None]], np.r_[pos[r], m]
-            want, w, top = attend(s.spec, q[r][None], k[r], v[r], [m], pos[r], causal=False)
-            reach = max(reach, top)
-            compare(got[r], want[0], s.dtype)
-            total[r] = (decay * np.r_[total[r], np.zeros((1, s.hkv))] if spare_mass else 0.0) + w
-        check_mass(new[:-1].cpu().numpy(), s.mass_of(total), reach, s.mode in ("prerotated", "doc_local"))
+            want = attend(s.spec, q[r][None], k[r], v[r], [m], pos[r], causal=False)
+            reach = max(reach, want.reach)
+            check_out(got[r], want, s.dtype, s.rounded, 0)
+            total[r] = (decay * np.r_[total[r], np.zeros((1, s.hkv))] if spare_mass else 0.0) + want.mass
+        check_mass(new[:-1].cpu().numpy(), s.mass_of(total), reach, s.rounded)
     assert s.pool.device_status() == 0
 
 
@@ -318,8 +318,8 @@ def test_decode_mass_without_a_slot(L):
     got = mass.cpu().numpy()
     np.testing.assert_array_equal(got[:4], before[:4])
     assert np.all(out[0].float().cpu().numpy() == 0)
-    _, w, reach = attend(s.spec, q[1][None], np.r_[s.k[1], kn[1][None]], np.r_[s.v[1], vn[1][None]], [25], np.arange(26))
-    check_mass(got, s.mass_of([np.full((56, s.hkv), 0.75), w + 0.25 * (np.arange(26) < 25)[:, None]]), reach)
+    ref = attend(s.spec, q[1][None], np.r_[s.k[1], kn[1][None]], np.r_[s.v[1], vn[1][None]], [25], np.arange(26))
+    check_mass(got, s.mass_of([np.full((56, s.hkv), 0.75), ref.mass + 0.25 * (np.arange(26) < 25)[:, None]]), ref.reach)
     assert s.pool.device_status() == L.LAZYATTN_ENODECODE
 
 
@@ -560,13 +560,13 @@ def test_a_cache_kept_small(L):
                     held[r][h] = np.r_[k, kn[r, h][None]], np.r_[v, vn[r, h][None]]
                     k, v = held[r][h]
                     g = s.hq // hkv
-                    want, w, reach = attend(s.spec, q[r, h * g:(h + 1) * g][None], k[:, None], v[:, None], [len(k) - 1],
+                    want = attend(s.spec, q[r, h * g:(h + 1) * g][None], k[:, None], v[:, None], [len(k) - 1],
                                             np.arange(len(k)))
-                    compare(got[r, h * g:(h + 1) * g], want[0], "bf16")
+                    check_out(got[r, h * g:(h + 1) * g], want, "bf16", row=0)
                     e0 = batch.offsets_host[r]
                     seen = add[e0:batch.offsets_host[r + 1], h].reshape(-1)
                     # the difference of two float32 totals below 256: half a step of each
-                    assert np.max(np.abs(seen[:len(k)] - w[:, 0])) <= 2.0 ** -16 + reach * 1e-5
+                    assert np.max(np.abs(seen[:len(k)] - want.mass[:, 0])) <= 2.0 ** -16 + want.reach * 1e-5
                     assert np.all(seen[len(k):] == 0)
     wn = L.lazyattn_window_workspace_size(s.pool.handle, L.LAZYATTN_OP_DECODE, batch.c, 20, 4)
     wsw = torch.zeros(wn, dtype=torch.uint8, device="cuda")
@@ -577,8 +577,8 @@ def test_a_cache_kept_small(L):
     for r in range(R):
         k = np.stack([np.r_[held[r][h][0], kn[r, h][None]] for h in range(hkv)], 1)
         v = np.stack([np.r_[held[r][h][1], vn[r, h][None]] for h in range(hkv)], 1)
-        want, _, _ = attend(s.spec, q[r][None], k, v, [len(k) - 1], np.arange(len(k)), 20, 4)
-        compare(got[r], want[0], "bf16")
+        want = attend(s.spec, q[r][None], k, v, [len(k) - 1], np.arange(len(k)), 20, 4)
+        check_out(got[r], want, "bf16", row=0)
     assert s.pool.device_status() == 0
     assert s.pool.free_count() < free0
 
