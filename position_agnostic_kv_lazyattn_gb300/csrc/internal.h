@@ -146,6 +146,7 @@ struct DecodeWs {
     int splits;
     // windowed decode: live entries per request, their lists, and (doc-local pools) their document offsets
     size_t count_off = 0, list_off = 0, delta_off = 0;
+    size_t score_off = 0;   // decode with mass: float [R][max_entries][Hkv][16][g]
 };
 
 // Live lists of a windowed decode step: request r's entries with a visible token,
@@ -246,6 +247,12 @@ DecodeWs decode_window_ws_layout(const lazyattn_pool& p, const lazyattn_batch& b
 int launch_decode_window_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
                               const void* k_new, const void* v_new, __nv_bfloat16* out, int32_t window, int32_t sinks,
                               void* ws, const DecodeWs& L, cudaStream_t stream);
+
+// bf16 decode step with its attention mass.
+DecodeWs decode_mass_ws_layout(const lazyattn_pool& p, const lazyattn_batch& b);
+int launch_decode_mass_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q, const void* k_new,
+                            const void* v_new, __nv_bfloat16* out, const float* mass_in, float* mass_out, float decay,
+                            void* ws, const DecodeWs& L, cudaStream_t stream);
 
 // bf16 decode through a plan: document-major units on tcgen05 / TMEM, then a
 // combine of each request's partial results.

@@ -25,7 +25,17 @@
 // Warps combine through shared memory; splits combine through a partial buffer
 // in the workspace, reduced by the last CTA of each (r, h) to arrive (atomic
 // ticket, nobody waits). Under a window (WIN) the pages are those of the request's
-// live list, written by the append kernel: the table's entries with a visible token. Every wait on a TMA is bounded; on a timeout the warp
+// live list, written by the append kernel: the table's entries with a visible token.
+//
+// With the step's attention mass (MASS4, MASS8) the scores are held to fp32 accuracy:
+// fp16 operands alone would leave 2^-11 relative errors on q and k, some 3e-4 on a
+// weight. So rotated q and k each go in as hi + lo, two fp16 numbers (lo the
+// rounding of the rest), and the score is K_hi Q_hi + (K_hi Q_lo + K_lo Q_hi), the
+// bracket in an accumulator of its own. A group of up to four heads puts Q_hi and Q_lo side
+// by side in the MMA's eight columns (MASS4: two MMAs a step, K_hi and K_lo); a larger one
+// takes three (MASS8, Q_lo from shared memory). The scores go to the workspace and
+// the splits' partials always do; mass_kernel, launched behind, merges the
+// statistics and the outputs and turns the scores into weights. Every wait on a TMA is bounded; on a timeout the warp
 // drains its copies and the CTA records LAZYATTN_EDEVICE.
 #include <limits.h>
 
@@ -66,7 +76,11 @@ struct DecodeParams {
     const int32_t* counts;        // WIN: live entries of each request; entries and entry_delta are then lists
     int32_t list_cap;             // of list_cap places a request
     int32_t window, sinks;
+    float* scores;                // MASS: [R][list_cap][Hkv][16][g], log2 domain
 };
+
+enum Kind { PLAIN, WINDOW, MASS4, MASS8 };
+constexpr int kQloBytes = 8 * 32 * 8;             // MASS8: Q_lo fragments, one uint2 per (k-step, lane)
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
@@ -157,14 +171,24 @@ __device__ __forceinline__ void compose2(float2 c1, float2 s1, float2 c2, float2
     c = f2_sub(f2_mul(c1, c2), f2_mul(s1, s2));
     s = f2_fma(s1, c2, f2_mul(c1, s2));
 }
+// What the fp16 pair `hi` leaves of (a, b), rounded to fp16: a + b to 22 bits or more.
+__device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return pack_h2(a - f.x, b - f.y);
+}
 // Rotate dims (d, d+1) [bf16x2 x] and their rotate-half partners (d+64, d+65)
-// [bf16x2 y] by angles with cosines c and sines s; fp16x2 out.
-__device__ __forceinline__ void rotate2v(uint32_t& x, uint32_t& y, float2 c, float2 s) {
+// [bf16x2 y] by angles with cosines c and sines s; fp16x2 out, and with REST what it leaves in rx, ry.
+template <bool REST>
+__device__ __forceinline__ void rotate2v(uint32_t& x, uint32_t& y, float2 c, float2 s, uint32_t& rx, uint32_t& ry) {
     const float2 a = make_float2(bf_lo(x), bf_hi(x)), b = make_float2(bf_lo(y), bf_hi(y));
     const float2 u = f2_sub(f2_mul(a, c), f2_mul(b, s));
     const float2 v = f2_fma(a, s, f2_mul(b, c));
     x = pack_h2(u.x, u.y);
     y = pack_h2(v.x, v.y);
+    if (REST) {
+        rx = rest_h2(u.x, u.y, x);
+        ry = rest_h2(v.x, v.y, y);
+    }
 }
 
 // 16-byte unit f4 (frequencies 2*f4, 2*f4+1) of slot-table row t. Odd rows swap
@@ -177,12 +201,14 @@ __device__ __forceinline__ int slot_unit(int t, int f4) { return t * (kRowBytes 
 // (its position relative to the page's document), once per change of delta
 // (§3.2 "Decoding": rotate q per document rather than K per token).
 // ALIBI: no rotation of q or k; each score gets -slope_h (m - n) (§3.5).
-// WIN: pages from the live lists; key n is visible iff n <= m and (m - n < window or n < sinks).
-template <bool PREROT, bool LOCAL, bool ALIBI, bool WIN>
+// WINDOW: pages from the live lists; key n is visible iff n <= m and (m - n < window or n < sinks).
+// MASS4 / MASS8: scores to fp32 accuracy, written out (groups of up to 4 / 8 heads).
+template <bool PREROT, bool LOCAL, bool ALIBI, Kind KIND>
 __global__ void __launch_bounds__(kThreads, 3)
     decode_bf16_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        PoolView pv, DecodeParams P) {
     constexpr bool ROT_K = !PREROT && !LOCAL && !ALIBI;   // keys rotated here
+    constexpr bool WIN = KIND == WINDOW, MASS = KIND >= MASS4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t bar_full[kWarps][kStages];
@@ -215,10 +241,11 @@ __global__ void __launch_bounds__(kThreads, 3)
     __syncthreads();
     int m = -1;   // logical position of the appended token: read from the append after grid_dep_wait()
 
-    int cb = 0, n_w = 0;                      // this CTA's first entry; pages of this warp
+    int first_entry = 0, cb = 0, n_w = 0;     // the request's first entry, this CTA's; pages of this warp
     const uint64_t* my_entries = P.entries;   // page i of this warp: my_entries[kWarps * i]
     auto share = [&](int e0, int e1) {
         const int chunk = (e1 - e0 + S - 1) / S;
+        first_entry = e0;
         cb = e0 + s * chunk;
         const int ce = min(e1, cb + chunk);
         n_w = ce - cb > warp ? (ce - cb - warp + kWarps - 1) / kWarps : 0;
@@ -282,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 3)
             if (early0 && 0 < n_w && page_n(e_cur, 0) > 0) mbar_wait(smem_u32(&bar_full[warp][0]), 0, &never);
             if (early1 && 1 < n_w && page_n(e_n1, 0) > 0) mbar_wait(smem_u32(&bar_full[warp][1]), 0, &never);
         }
-        if (s == 0)
+        if (!MASS && s == 0)
             for (int i = tid; i < g * kD; i += kThreads) out_rh[i] = __float2bfloat16_rn(0.f);
         return;
     }
@@ -303,20 +330,34 @@ __global__ void __launch_bounds__(kThreads, 3)
     int last_delta = INT_MIN;
     bool q_range_ok = true;        // input range: rotated, scaled pairs must stay finite in fp16
     const float qsc2 = (kLog2e * pv.qk_scale) * (kLog2e * pv.qk_scale);
+    const int head = KIND == MASS4 ? gr & 3 : gr;   // the head of this lane's B column; MASS4: columns 4..7 are Q_lo
+    // MASS8: Q_lo fragments (doc-local: each warp's own, its document's)
+    uint2* qlo = reinterpret_cast<uint2*>(sm + kSmemBytes - 1024 + (LOCAL ? warp * kQloBytes : 0)) + lane;
+    // k-step t, half hf: the fp16 pair of (a, b); MASS: its hi or lo part
+    auto put_q = [&](int t, int hf, float a, float b) {
+        const uint32_t hi = pack_h2(a, b);
+        if (!MASS) {
+            qb[t][hf] = hi;
+            return;
+        }
+        const uint32_t lo = rest_h2(a, b, hi);
+        qb[t][hf] = KIND == MASS4 && gr >= 4 ? lo : hi;
+        if (KIND == MASS8) reinterpret_cast<uint32_t*>(qlo + 32 * t)[hf] = lo;   // every warp writes the same
+    };
     auto check_q = [&](uint32_t x, uint32_t y) {
         const float a0 = bf_lo(x), a1 = bf_hi(x), b0 = bf_lo(y), b1 = bf_hi(y);
         const float n2 = fmaxf(fmaf(a0, a0, b0 * b0), fmaf(a1, a1, b1 * b1));
         q_range_ok = q_range_ok && (n2 * qsc2 <= kMaxPairNorm2);
     };
     if (LOCAL) {
-        const uint32_t* qp = reinterpret_cast<const uint32_t*>(P.q + ((size_t)r * Hq + (size_t)h * g + min(gr, g - 1)) * kD);
+        const uint32_t* qp = reinterpret_cast<const uint32_t*>(P.q + ((size_t)r * Hq + (size_t)h * g + min(head, g - 1)) * kD);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int d = 16 * t + 2 * c + 8 * hf;
-                uint32_t x = gr < g ? __ldg(qp + (pv.interleaved ? d : d / 2)) : 0u;
-                uint32_t y = gr < g ? __ldg(qp + (pv.interleaved ? d + 1 : (d + 64) / 2)) : 0u;
+                uint32_t x = head < g ? __ldg(qp + (pv.interleaved ? d : d / 2)) : 0u;
+                uint32_t y = head < g ? __ldg(qp + (pv.interleaved ? d + 1 : (d + 64) / 2)) : 0u;
                 if (pv.interleaved) {   // (2d, 2d+1), (2d+2, 2d+3) -> dims (d, d+1) and (d+64, d+65)
                     const uint32_t p0 = x, p1 = y;
                     x = __byte_perm(p0, p1, 0x5410);
@@ -324,12 +365,12 @@ __global__ void __launch_bounds__(kThreads, 3)
                 }
                 qx[t][hf] = x;
                 qy[t][hf] = y;
-                if (gr < g) check_q(x, y);
+                if (head < g) check_q(x, y);
             }
 #pragma unroll
         for (int t = 0; t < 8; ++t) qb[t][0] = qb[t][1] = 0u;
-    } else if (gr < g) {
-        const uint32_t* qp = reinterpret_cast<const uint32_t*>(P.q + ((size_t)r * Hq + (size_t)h * g + gr) * kD);
+    } else if (head < g) {
+        const uint32_t* qp = reinterpret_cast<const uint32_t*>(P.q + ((size_t)r * Hq + (size_t)h * g + head) * kD);
         const float4* row = reinterpret_cast<const float4*>(pv.rope + (size_t)m * (kD / 2));
         const float sc = kLog2e * pv.qk_scale;
 #pragma unroll
@@ -346,20 +387,24 @@ __global__ void __launch_bounds__(kThreads, 3)
                 check_q(x, y);
                 const float4 cs = ALIBI ? make_float4(1.f, 0.f, 1.f, 0.f) : __ldg(row + d / 2);
                 const float a0 = bf_lo(x), a1 = bf_hi(x), b0 = bf_lo(y), b1 = bf_hi(y);
-                qb[t][hf] = pack_h2((a0 * cs.x - b0 * cs.y) * sc, (a1 * cs.z - b1 * cs.w) * sc);
-                qb[t + 4][hf] = pack_h2((a0 * cs.y + b0 * cs.x) * sc, (a1 * cs.w + b1 * cs.z) * sc);
+                put_q(t, hf, (a0 * cs.x - b0 * cs.y) * sc, (a1 * cs.z - b1 * cs.w) * sc);
+                put_q(t + 4, hf, (a0 * cs.y + b0 * cs.x) * sc, (a1 * cs.w + b1 * cs.z) * sc);
             }
         }
     } else {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) qb[t][0] = qb[t][1] = 0u;
+        for (int t = 0; t < 8; ++t) {
+            qb[t][0] = qb[t][1] = 0u;
+            if (KIND == MASS8) qlo[32 * t] = make_uint2(0u, 0u);
+        }
     }
 
     if (!q_range_ok && s == 0) record_error(pv.status, LAZYATTN_ERANGE);
 
     // ALiBi slopes of this lane's two heads, in the log2 domain of the scores
-    const float al0 = ALIBI ? alibi_slope(h * g + min(2 * c, g - 1), Hq) * kLog2e : 0.f;
-    const float al1 = ALIBI ? alibi_slope(h * g + min(2 * c + 1, g - 1), Hq) * kLog2e : 0.f;
+    const int hc = KIND == MASS4 ? 2 * (c & 1) : 2 * c;   // the heads of this lane's score columns: hc, hc + 1
+    const float al0 = ALIBI ? alibi_slope(h * g + min(hc, g - 1), Hq) * kLog2e : 0.f;
+    const float al1 = ALIBI ? alibi_slope(h * g + min(hc + 1, g - 1), Hq) * kLog2e : 0.f;
 
     float o[8][4];
 #pragma unroll
@@ -396,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 3)
                         const float2 cc = make_float2(b4.x * sc, b4.y * sc), ss = make_float2(b4.z * sc, b4.w * sc);
                         const float2 u = f2_sub(f2_mul(a, cc), f2_mul(b, ss));
                         const float2 v = f2_fma(a, ss, f2_mul(b, cc));
-                        qb[t][hf] = pack_h2(u.x, u.y);
-                        qb[t + 4][hf] = pack_h2(v.x, v.y);
+                        put_q(t, hf, u.x, u.y);
+                        put_q(t + 4, hf, v.x, v.y);
                     }
             }
             if (!mbar_wait(smem_u32(&bar_full[warp][st]), (phases >> st) & 1u, abort_flag)) break;
@@ -409,9 +454,11 @@ __global__ void __launch_bounds__(kThreads, 3)
             // partners (dims 16t+.. and 64+16t+..), so they are loaded, rotated and
             // multiplied together: (tokens gr | gr+8) x (dims 16t+2c.. | 16t+2c+8..)
             float sacc[4] = {0.f, 0.f, 0.f, 0.f};
+            float rest[4] = {0.f, 0.f, 0.f, 0.f};   // MASS: the products with a lo part (MASS4: with K_lo)
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                uint32_t lo[4], hi[4];
+                uint32_t lo[4], hi[4];       // dims 16t.. of the first and of the second half
+                uint32_t rlo[4], rhi[4];     // MASS: the lo parts of both
                 const int row = lane & 15, unit = (t & 3) * 2 + (lane >> 4);
                 ldsm_x4(lo, stg + row * 128 + ((unit ^ (row & 7)) << 4));
                 ldsm_x4(hi, stg + 2048 + row * 128 + ((unit ^ (row & 7)) << 4));
@@ -427,18 +474,46 @@ __global__ void __launch_bounds__(kThreads, 3)
                         compose2(make_float2(b4.x, b4.y), make_float2(b4.z, b4.w), make_float2(x.x, x.y),
                                  make_float2(x.z, x.w), cac, cas);
                         compose2(cac, cas, make_float2(y.x, y.y), make_float2(y.z, y.w), cbc, cbs);
-                        rotate2v(lo[2 * hf], hi[2 * hf], cac, cas);
-                        rotate2v(lo[2 * hf + 1], hi[2 * hf + 1], cbc, cbs);
+                        rotate2v<MASS>(lo[2 * hf], hi[2 * hf], cac, cas, rlo[2 * hf], rhi[2 * hf]);
+                        rotate2v<MASS>(lo[2 * hf + 1], hi[2 * hf + 1], cbc, cbs, rlo[2 * hf + 1], rhi[2 * hf + 1]);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        lo[j] = bf2_to_h2(lo[j]);
-                        hi[j] = bf2_to_h2(hi[j]);
+                        const uint32_t a = lo[j], b = hi[j];
+                        lo[j] = bf2_to_h2(a);
+                        hi[j] = bf2_to_h2(b);
+                        if (MASS) {   // a bf16 number below fp16's normal range leaves a rest
+                            rlo[j] = rest_h2(bf_lo(a), bf_hi(a), lo[j]);
+                            rhi[j] = rest_h2(bf_lo(b), bf_hi(b), hi[j]);
+                        }
                     }
                 }
                 mma_f16(sacc, lo[0], lo[1], lo[2], lo[3], qb[t][0], qb[t][1]);
                 mma_f16(sacc, hi[0], hi[1], hi[2], hi[3], qb[t + 4][0], qb[t + 4][1]);
+                if (MASS) {
+                    mma_f16(rest, rlo[0], rlo[1], rlo[2], rlo[3], qb[t][0], qb[t][1]);
+                    mma_f16(rest, rhi[0], rhi[1], rhi[2], rhi[3], qb[t + 4][0], qb[t + 4][1]);
+                }
+                if (KIND == MASS8) {
+                    const uint2 q0 = qlo[32 * t], q1 = qlo[32 * (t + 4)];
+                    mma_f16(rest, lo[0], lo[1], lo[2], lo[3], q0.x, q0.y);
+                    mma_f16(rest, hi[0], hi[1], hi[2], hi[3], q1.x, q1.y);
+                }
+            }
+            if (MASS) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (KIND == MASS4) {
+                        // columns n and n + 4 (lanes c and c ^ 2) are the same head's Q_hi and Q_lo; both lanes
+                        // form K_hi Q_hi + (K_lo Q_hi + (K_hi Q_lo + K_lo Q_lo)), the small ones first
+                        const float other = __shfl_xor_sync(0xffffffffu, c < 2 ? sacc[j] : sacc[j] + rest[j], 2);
+                        const float other_rest = __shfl_xor_sync(0xffffffffu, rest[j], 2);
+                        sacc[j] = c < 2 ? sacc[j] + (rest[j] + other) : other + (other_rest + (sacc[j] + rest[j]));
+                    } else {
+                        sacc[j] += rest[j];
+                    }
+                }
             }
 
             // S^T fragment: (token gr | gr+8) x (head 2c | 2c+1)
@@ -454,6 +529,20 @@ __global__ void __launch_bounds__(kThreads, 3)
                 sacc[1] += al1 * dn;
                 sacc[2] += al0 * (dn + 8.f);
                 sacc[3] += al1 * (dn + 8.f);
+            }
+            if (MASS && hc < g && (KIND == MASS8 || c < 2)) {
+                float* to = P.scores + ((((size_t)r * P.list_cap + (cb - first_entry) + warp + kWarps * i) * Hkv + h) * kPage + gr) * g + hc;
+                if ((g & 1) == 0) {
+                    *reinterpret_cast<float2*>(to) = make_float2(sacc[0], sacc[1]);
+                    *reinterpret_cast<float2*>(to + 8 * g) = make_float2(sacc[2], sacc[3]);
+                } else {
+                    to[0] = sacc[0];
+                    to[8 * g] = sacc[2];
+                    if (hc + 1 < g) {
+                        to[1] = sacc[1];
+                        to[8 * g + 1] = sacc[3];
+                    }
+                }
             }
             const float s0 = v0 ? sacc[0] : -INFINITY;
             const float s1 = v0 ? sacc[1] : -INFINITY;
@@ -573,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
     }
 
-    if (S == 1) {
+    if (!MASS && S == 1) {
         if (hh < g) {
             const float inv = L > 0.f ? 1.f / L : 0.f;
             uint4 w;
@@ -594,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         dst[0] = make_float4(a[0], a[1], a[2], a[3]);
         dst[1] = make_float4(a[4], a[5], a[6], a[7]);
     }
+    if (MASS) return;   // mass_kernel merges the partials
     __threadfence();
     __syncthreads();
     if (tid == 0) s_last = (atomicAdd(&P.tickets[rh], 1) == S - 1) ? 1 : 0;
@@ -629,6 +719,87 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (tid == 0) P.tickets[rh] = 0;
 }
 
+// Behind a MASS launch. Block = (32 entries, KV head, request): the splits' statistics of
+// the group's heads (one warp a head, one lane a split) give each head's largest score
+// and 1 / sum; the first block also merges the outputs; then thread = (entry,
+// slot) turns its g scores into weights. The scores were written just before: they
+// are read once, mostly from L2.
+constexpr int kMassThreads = 256;
+constexpr int kMassEntries = 32;
+template <bool LOCAL>
+__global__ void __launch_bounds__(kMassThreads)
+    mass_kernel(PoolView pv, DecodeParams P, const float* mass_in, float* mass_out, float decay) {
+    __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
+    const int r = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = P.g, S = P.splits;
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int e0 = P.entry_offsets[r], E = P.entry_offsets[r + 1] - e0;
+    const int m = P.qpos[r];
+    const size_t rh = (size_t)r * pv.hkv + h;
+    if (m >= 0 && warp < g) {
+        const float2 x = lane < S ? P.ml[(rh * S + lane) * g + warp] : make_float2(-INFINITY, 0.f);
+        float M = x.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float wt = M == -INFINITY ? 0.f : fast_exp2(x.x - M);
+        float L = x.y * wt;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        if (lane == 0) {
+            s_m[warp] = M == -INFINITY ? 0.f : M;
+            s_inv[warp] = inv;
+        }
+        if (blockIdx.x == 0) {   // lane = 4 dims of the head's output
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int t = 0; t < S; ++t) {
+                const float w = __shfl_sync(0xffffffffu, wt, t) * inv;
+                const float4 y = reinterpret_cast<const float4*>(P.acc + ((rh * S + t) * g + warp) * kD)[lane];
+                a.x += y.x * w; a.y += y.y * w; a.z += y.z * w; a.w += y.w * w;
+            }
+            reinterpret_cast<uint2*>(P.out + ((size_t)r * pv.hq + (size_t)h * g + warp) * kD)[lane] =
+                make_uint2(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w));
+        }
+    } else if (warp < g && blockIdx.x == 0) {
+        reinterpret_cast<uint2*>(P.out + ((size_t)r * pv.hq + (size_t)h * g + warp) * kD)[lane] = make_uint2(0u, 0u);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMassEntries; k += kMassThreads / kPage) {
+        const int i = (int)blockIdx.x * kMassEntries + k + (tid >> 4), slot = tid & 15;
+        if (i >= E) break;
+        const uint64_t e = P.entries[e0 + i];
+        int n = usable_tokens(pv, e);
+        if (LOCAL && n > 0) {
+            const int d = P.entry_delta[e0 + i];
+            if (d < 0 || d > entry_start(e) || (m >= 0 && (m - d < 0 || m - d >= pv.max_position))) n = 0;
+        }
+        const size_t at = ((size_t)(e0 + i) * pv.hkv + h) * kPage + slot;
+        float sum = 0.f;
+        if (slot < n) {
+            if (m >= 0) {
+                const float* s = P.scores + (((size_t)r * P.list_cap + i) * pv.hkv + h) * (kPage * g) + slot * g;
+                if (g == 8) {
+                    const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
+                    sum = fast_exp2(a.x - s_m[0]) * s_inv[0] + fast_exp2(a.y - s_m[1]) * s_inv[1] +
+                          fast_exp2(a.z - s_m[2]) * s_inv[2] + fast_exp2(a.w - s_m[3]) * s_inv[3] +
+                          fast_exp2(b.x - s_m[4]) * s_inv[4] + fast_exp2(b.y - s_m[5]) * s_inv[5] +
+                          fast_exp2(b.z - s_m[6]) * s_inv[6] + fast_exp2(b.w - s_m[7]) * s_inv[7];
+                } else if (g == 4) {
+                    const float4 a = *reinterpret_cast<const float4*>(s);
+                    sum = fast_exp2(a.x - s_m[0]) * s_inv[0] + fast_exp2(a.y - s_m[1]) * s_inv[1] +
+                          fast_exp2(a.z - s_m[2]) * s_inv[2] + fast_exp2(a.w - s_m[3]) * s_inv[3];
+                } else {
+                    for (int j = 0; j < g; ++j) sum += fast_exp2(s[j] - s_m[j]) * s_inv[j];
+                }
+            }
+            if (mass_in) sum += m >= 0 ? decay * mass_in[at] : mass_in[at];
+        }
+        mass_out[at] = sum;
+    }
+}
+
 // Splits per (request, KV head). Cost model in units of one page per warp:
 // every wave of CTAs pays a fixed overhead (prologue, pipeline fill, the
 // combine) plus its CTAs' longest page run, so
@@ -661,22 +832,35 @@ inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 using DecodeKernel = void (*)(const CUtensorMap, const CUtensorMap, PoolView, DecodeParams);
 
-template <bool WIN>
+template <Kind KIND>
 static DecodeKernel decode_kernel_variant(bool prerot, bool local, bool alibi) {
-    if (alibi) return decode_bf16_kernel<false, false, true, WIN>;
-    if (local) return decode_bf16_kernel<false, true, false, WIN>;
-    return prerot ? decode_bf16_kernel<true, false, false, WIN> : decode_bf16_kernel<false, false, false, WIN>;
+    if (alibi) return decode_bf16_kernel<false, false, true, KIND>;
+    if (local) return decode_bf16_kernel<false, true, false, KIND>;
+    return prerot ? decode_bf16_kernel<true, false, false, KIND> : decode_bf16_kernel<false, false, false, KIND>;
+}
+
+static DecodeKernel decode_kernel_for(Kind kind, bool prerot, bool local, bool alibi) {
+    switch (kind) {
+        case WINDOW: return decode_kernel_variant<WINDOW>(prerot, local, alibi);
+        case MASS4: return decode_kernel_variant<MASS4>(prerot, local, alibi);
+        case MASS8: return decode_kernel_variant<MASS8>(prerot, local, alibi);
+        default: return decode_kernel_variant<PLAIN>(prerot, local, alibi);
+    }
+}
+
+static size_t smem_bytes(Kind kind, bool local) {
+    return kSmemBytes + (kind == MASS8 ? (local ? kWarps : 1) * kQloBytes : 0);
 }
 
 int decode_occupancy(int* ctas_per_sm) {
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
         const bool prerot = (i & 3) == 1, local = (i & 3) == 2, alibi = (i & 3) == 3;
-        DecodeKernel k = i < 4 ? decode_kernel_variant<false>(prerot, local, alibi)
-                               : decode_kernel_variant<true>(prerot, local, alibi);
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+        const Kind kind = static_cast<Kind>(i >> 2);
+        if (cudaFuncSetAttribute(decode_kernel_for(kind, prerot, local, alibi), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem_bytes(kind, local)) != cudaSuccess)
             return LAZYATTN_ECUDA;
     }
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_bf16_kernel<false, false, false, false>,
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, decode_bf16_kernel<false, false, false, PLAIN>,
                                                          kThreads, kSmemBytes) == cudaSuccess
                ? LAZYATTN_OK
                : LAZYATTN_ECUDA;
@@ -730,22 +914,21 @@ static DecodeParams decode_params(const lazyattn_pool& p, const lazyattn_batch& 
     return P;
 }
 
-static int launch(const lazyattn_pool& p, const lazyattn_batch& b, const DecodeParams& P, bool win, cudaStream_t stream) {
+static int launch(const lazyattn_pool& p, const lazyattn_batch& b, const DecodeParams& P, Kind kind, cudaStream_t stream) {
     if (!p.have_maps) return LAZYATTN_ECUDA;
     const bool prerot = (b.flags & LAZYATTN_KEYS_PREROTATED) != 0;
     const bool local = p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL;
     const bool alibi = p.d.position_encoding == LAZYATTN_POS_ALIBI;
-    DecodeKernel kern = win ? decode_kernel_variant<true>(prerot, local, alibi)
-                            : decode_kernel_variant<false>(prerot, local, alibi);
+    DecodeKernel kern = decode_kernel_for(kind, prerot, local, alibi);
     const dim3 grid(P.splits, p.d.n_kv_heads, b.num_requests);
-    if (launch_dependent(kern, grid, dim3(kThreads), kSmemBytes, stream, p.kmap, p.vmap, p.view(), P) != cudaSuccess)
+    if (launch_dependent(kern, grid, dim3(kThreads), smem_bytes(kind, local), stream, p.kmap, p.vmap, p.view(), P) != cudaSuccess)
         return LAZYATTN_ECUDA;
     return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;
 }
 
 int launch_decode_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
                        __nv_bfloat16* out, void* ws, const DecodeWs& L, cudaStream_t stream) {
-    return launch(p, b, decode_params(p, b, q, out, static_cast<char*>(ws), L), false, stream);
+    return launch(p, b, decode_params(p, b, q, out, static_cast<char*>(ws), L), PLAIN, stream);
 }
 
 int launch_decode_window_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
@@ -769,7 +952,33 @@ int launch_decode_window_bf16(const lazyattn_pool& p, const lazyattn_batch& b, c
     P.list_cap = lists.cap;
     P.window = window;
     P.sinks = sinks;
-    return launch(p, b, P, true, stream);
+    return launch(p, b, P, WINDOW, stream);
+}
+
+DecodeWs decode_mass_ws_layout(const lazyattn_pool& p, const lazyattn_batch& b) {
+    DecodeWs L = decode_ws_layout(p, b);
+    L.score_off = L.total;
+    const size_t places = (size_t)b.num_requests * (size_t)std::max(b.max_entries, 1);
+    L.total += up256(places * (size_t)p.d.n_q_heads * kPage * sizeof(float));
+    return L;
+}
+
+int launch_decode_mass_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q, const void* k_new,
+                            const void* v_new, __nv_bfloat16* out, const float* mass_in, float* mass_out, float decay,
+                            void* ws, const DecodeWs& L, cudaStream_t stream) {
+    char* base = static_cast<char*>(ws);
+    int rc = launch_decode_append(p, b, k_new, v_new, reinterpret_cast<int32_t*>(base + L.qpos_off), stream);
+    if (rc != LAZYATTN_OK) return rc;
+    DecodeParams P = decode_params(p, b, q, out, base, L);
+    P.list_cap = std::max(b.max_entries, 1);
+    P.scores = reinterpret_cast<float*>(base + L.score_off);
+    rc = launch(p, b, P, P.g <= 4 ? MASS4 : MASS8, stream);
+    if (rc != LAZYATTN_OK) return rc;
+    const dim3 grid((P.list_cap + kMassEntries - 1) / kMassEntries, p.d.n_kv_heads, b.num_requests);
+    auto kern = p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL ? mass_kernel<true> : mass_kernel<false>;
+    if (launch_dependent(kern, grid, dim3(kMassThreads), 0, stream, p.view(), P, mass_in, mass_out, decay) != cudaSuccess)
+        return LAZYATTN_ECUDA;
+    return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;
 }
 
 }  // namespace lazyattn

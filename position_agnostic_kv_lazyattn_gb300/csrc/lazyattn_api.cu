@@ -367,6 +367,7 @@ size_t lazyattn_workspace_size(lazyattn_pool_t pool, int32_t op, const lazyattn_
         return prefill_bytes(pool, batch, INT32_MAX, 0);
     }
     if (op == LAZYATTN_OP_PREFILL_MASS) return mass_simt_ws_bytes(*pool, batch->total_q) + 256;
+    if (op == LAZYATTN_OP_DECODE_MASS && pool->d.dtype == LAZYATTN_BF16) return decode_mass_ws_layout(*pool, *batch).total;
     if (op == LAZYATTN_OP_DECODE_MASS) return qpos_bytes(batch) + mass_simt_ws_bytes(*pool, batch->num_requests);
     if (op != LAZYATTN_OP_DECODE) return 0;
     if (pool->d.dtype == LAZYATTN_F32) return (size_t)batch->num_requests * sizeof(int32_t) + 256;
@@ -502,6 +503,10 @@ int lazyattn_decode_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, cons
     rc = check_device(pool);
     if (rc != LAZYATTN_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pool->d.dtype == LAZYATTN_BF16)
+        return launch_decode_mass_bf16(*pool, *batch, static_cast<const __nv_bfloat16*>(q), k_new, v_new,
+                                       static_cast<__nv_bfloat16*>(out), mass_in, mass_out, decay, workspace,
+                                       decode_mass_ws_layout(*pool, *batch), st);
     int32_t* qpos = static_cast<int32_t*>(workspace);
     rc = launch_decode_append(*pool, *batch, k_new, v_new, qpos, st);
     if (rc != LAZYATTN_OK) return rc;
