@@ -278,7 +278,13 @@ int launch_prefill_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const _
 int launch_window_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void* q, void* out,
                        const int32_t* decode_qpos, int32_t window, int32_t sinks, cudaStream_t stream);
 
-// Attention mass on CUDA cores, and the rows' outputs unless out is NULL; ws holds
+// bf16 attention mass of the batch's query rows on tcgen05 / TMEM; ws holds mass_tc_ws_bytes.
+int mass_tc_init();
+size_t mass_tc_ws_bytes(const lazyattn_pool& p, const lazyattn_batch& b);
+int launch_prefill_mass_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
+                             const float* mass_in, float* mass_out, float decay, void* ws, cudaStream_t stream);
+
+// Attention mass of fp32 pools on CUDA cores, and the rows' outputs unless out is NULL; ws holds
 // mass_simt_ws_bytes for the number of query rows.
 size_t mass_simt_ws_bytes(const lazyattn_pool& p, int64_t rows);
 int launch_mass_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void* q, void* out,

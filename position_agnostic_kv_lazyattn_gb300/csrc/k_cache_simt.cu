@@ -1,7 +1,7 @@
-// Windowed attention and attention mass on CUDA cores, fp32 arithmetic end to
-// end, for either element type and every key layout and position encoding.
+// Windowed attention and attention mass of fp32 pools on CUDA cores, fp32 end to end
+// (position-free or pre-rotated keys, rotary encodings; other layouts are bf16 only).
 //
-//   score(row, token) = log2(e) * scale * (R_m q) . (R_n k)  [+ ALiBi], log2 domain
+//   score(row, token) = log2(e) * scale * (R_m q) . (R_n k), log2 domain
 //   out  = sum_n 2^(score - max) v_n / sum_n 2^(score - max)
 //   mass = decay * mass_in + sum over rows and the group's heads of
 //          2^(score - max_row) / sum_row
@@ -19,20 +19,10 @@ constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xffff0000u));
-}
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 struct Params {
     const uint64_t* entries;
     const int32_t* entry_offsets;
-    const int32_t* entry_delta;   // doc-local pools
     const int32_t* q_offsets;     // prefill
     const int32_t* q_start;
     const int32_t* decode_qpos;   // decode: position of the appended token, -1 if none (else NULL)
@@ -40,9 +30,7 @@ struct Params {
     int32_t max_rows;             // prefill: rows per request that rows_kernel covers
     int32_t window, sinks;
     int32_t causal;               // keys past the row's position are hidden
-    int32_t rotate_k;             // 0: as stored; 1: at start + slot; 2: by the document's offset (doc-local)
-    int32_t rotate_q;             // 0 with ALiBi
-    int32_t alibi;
+    int32_t rotate_k;             // 0: pre-rotated pages
     float2* stats;                // [row][Hq]: (largest score, 1 / sum), or NULL
     float* q_rot;                 // [row][Hq][D] rotated, scaled q, or NULL
 };
@@ -52,30 +40,19 @@ __device__ __forceinline__ bool visible(const Params& P, int n, int m) {
 }
 
 // Entry's usable slots: 0 for an empty or an unusable one (reported).
-__device__ __forceinline__ int slots_of(const PoolView& pv, const Params& P, int i, uint64_t e) {
-    if (!entry_ok(pv, e)) return 0;
-    const int n = entry_nvalid(e);
-    if (n > 0 && P.rotate_k == 2) {
-        const int d = P.entry_delta[i];
-        if (d < 0 || d > entry_start(e)) {
-            record_error(pv.status, LAZYATTN_ERANGE);
-            return 0;
-        }
-    }
-    return n;
-}
+__device__ __forceinline__ int slots_of(const PoolView& pv, uint64_t e) { return entry_ok(pv, e) ? entry_nvalid(e) : 0; }
 
 // This lane's part of its key (slot lane % 16): D / 4 pairs from dim (lane / 16) * D / 4
 // on, rotated to its position; x the first halves' dims, y their partners.
-template <typename T, int D>
-__device__ __forceinline__ void load_key(const PoolView& pv, const Params& P, const T* row, int rot_pos, int d0,
+template <int D>
+__device__ __forceinline__ void load_key(const PoolView& pv, const Params& P, const float* row, int pos, int d0,
                                          float (&x)[D / 4], float (&y)[D / 4]) {
 #pragma unroll
     for (int j = 0; j < D / 4; j += 4) {
         const float4 a = load4(row + d0 + j), b = load4(row + d0 + j + D / 2);
         const float xs[4] = {a.x, a.y, a.z, a.w}, ys[4] = {b.x, b.y, b.z, b.w};
         if (P.rotate_k) {
-            const float4* cs = reinterpret_cast<const float4*>(pv.rope + (size_t)rot_pos * (D / 2) + d0 + j);
+            const float4* cs = reinterpret_cast<const float4*>(pv.rope + (size_t)pos * (D / 2) + d0 + j);
             const float4 c0 = cs[0], c1 = cs[1];
             const float co[4] = {c0.x, c0.z, c1.x, c1.z}, si[4] = {c0.y, c0.w, c1.y, c1.w};
 #pragma unroll
@@ -108,8 +85,9 @@ __device__ __forceinline__ float dot_key(const float* q, int d0, const float (&x
 
 // Block = (query row, query head, request); its warps share the live entries.
 // out NULL: statistics only.
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) rows_kernel(PoolView pv, Params P, const T* __restrict__ q, T* out) {
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32)
+    rows_kernel(PoolView pv, Params P, const float* __restrict__ q, float* out) {
     constexpr int J = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.z, hq = blockIdx.y, i = blockIdx.x;
@@ -134,18 +112,15 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(PoolView pv, Params P
     if (m < 0 || m >= pv.max_position) {
         if (m >= 0 || !P.decode_qpos) record_error(pv.status, LAZYATTN_ERANGE);
         if (out)
-            for (int d = threadIdx.x; d < D; d += kWarps * 32) put(out + at * D + d, 0.f);
+            for (int d = threadIdx.x; d < D; d += kWarps * 32) out[at * D + d] = 0.f;
         if (P.stats && threadIdx.x == 0) P.stats[at] = make_float2(0.f, 0.f);
         if (P.q_rot)   // never NaN, its weights are 0 by the statistics
             for (int d = threadIdx.x; d < D; d += kWarps * 32) P.q_rot[at * D + d] = 0.f;
         return;
     }
     for (int d = threadIdx.x; d < D / 2; d += kWarps * 32) {
-        const T* qp = q + at * D;
-        const float a = to_f(qp[pv.interleaved ? 2 * d : d]), b = to_f(qp[pv.interleaved ? 2 * d + 1 : d + D / 2]);
-        const float sc = kLog2e * pv.qk_scale;
-        if (sizeof(T) == 2 && !((a * a + b * b) * sc * sc <= kMaxPairNorm2)) record_error(pv.status, LAZYATTN_ERANGE);
-        const float2 cs = P.rotate_q ? pv.rope[(size_t)m * (D / 2) + d] : make_float2(1.f, 0.f);
+        const float a = q[at * D + d], b = q[at * D + d + D / 2], sc = kLog2e * pv.qk_scale;
+        const float2 cs = pv.rope[(size_t)m * (D / 2) + d];
         const float x = (a * cs.x - b * cs.y) * sc, y = (a * cs.y + b * cs.x) * sc;
         s_q[d] = x;
         s_q[d + D / 2] = y;
@@ -156,10 +131,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(PoolView pv, Params P
     }
     __syncthreads();
 
-    const float slope = P.alibi ? alibi_slope(hq, pv.hq) * kLog2e : 0.f;
     const int slot = lane & 15, d0 = (lane >> 4) * (D / 4);
-    const T* kpool = static_cast<const T*>(pv.k_pool);
-    const T* vpool = static_cast<const T*>(pv.v_pool);
+    const float* kpool = static_cast<const float*>(pv.k_pool);
+    const float* vpool = static_cast<const float*>(pv.v_pool);
     float mx = -INFINITY, l = 0.f, acc[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) acc[j] = 0.f;
@@ -167,7 +141,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(PoolView pv, Params P
     int rank = 0;   // live entries before this chunk
     for (int c = e0; c < e1; c += 32) {
         const uint64_t mine = c + lane < e1 ? P.entries[c + lane] : 0ull;
-        const int n_mine = c + lane < e1 ? slots_of(pv, P, c + lane, mine) : 0;
+        const int n_mine = c + lane < e1 ? slots_of(pv, mine) : 0;
         const int a = entry_start(mine), b = a + n_mine - 1;
         const bool live = n_mine > 0 && (!P.causal || (a <= m && (m - b < P.window || a < P.sinks)));
         unsigned todo = __ballot_sync(0xffffffffu, live);
@@ -181,10 +155,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(PoolView pv, Params P
             const size_t base = ((size_t)entry_page(e) * pv.hkv + kvh) * kPage * D;
             const int use = slot < n ? slot : 0;
             float x[D / 4], y[D / 4];
-            load_key<T, D>(pv, P, kpool + base + (size_t)use * D,
-                           P.rotate_k == 2 ? P.entry_delta[c + src] : entry_start(e) + use, d0, x, y);
+            load_key<D>(pv, P, kpool + base + (size_t)use * D, entry_start(e) + use, d0, x, y);
             float s = dot_key<D>(s_q, d0, x, y);
-            s = see ? s - slope * (float)(m - pos) : -INFINITY;
+            s = see ? s : -INFINITY;
             float top = s;
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -204,7 +177,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(PoolView pv, Params P
                 if (t < n) {
 #pragma unroll
                     for (int j = 0; j < J; ++j)
-                        acc[j] = fmaf(pt, to_f(vpool[base + (size_t)t * D + lane + 32 * j]), acc[j]);
+                        acc[j] = fmaf(pt, vpool[base + (size_t)t * D + lane + 32 * j], acc[j]);
                 }
             }
         }
@@ -227,12 +200,12 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(PoolView pv, Params P
             float o = 0.f;
             if (M != -INFINITY)
                 for (int w = 0; w < kWarps; ++w) o += s_acc[w][d] * exp2f(s_m[w] - M);
-            put(out + at * D + d, o * inv);
+            out[at * D + d] = o * inv;
         }
 }
 
 // Warp = (entry, KV head, request): the mass of the entry's 16 slots over all rows.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kWarps * 32)
     mass_kernel(PoolView pv, Params P, const float* mass_in, float* mass_out, float decay) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -241,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (i >= P.entry_offsets[r + 1]) return;
     const int g = pv.hq / pv.hkv;
     const uint64_t e = P.entries[i];
-    const int n = slots_of(pv, P, i, e);
+    const int n = slots_of(pv, e);
     const int slot = lane & 15, d0 = (lane >> 4) * (D / 4);
     const int pos = entry_start(e) + slot;
     int row0, rows, m0;
@@ -258,9 +231,9 @@ __global__ void __launch_bounds__(kWarps * 32)
     float sum = 0.f;
     if (n > 0 && rows > 0) {
         const int use = slot < n ? slot : 0;
-        const T* row = static_cast<const T*>(pv.k_pool) + (((size_t)entry_page(e) * pv.hkv + h) * kPage + use) * D;
+        const float* row = static_cast<const float*>(pv.k_pool) + (((size_t)entry_page(e) * pv.hkv + h) * kPage + use) * D;
         float x[D / 4], y[D / 4];
-        load_key<T, D>(pv, P, row, P.rotate_k == 2 ? P.entry_delta[i] : entry_start(e) + use, d0, x, y);
+        load_key<D>(pv, P, row, entry_start(e) + use, d0, x, y);
         for (int t = 0; t < rows; ++t) {
             const int m = m0 + t;
             if (P.causal && m < entry_start(e)) continue;
@@ -268,8 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32)
             for (int j = 0; j < g; ++j) {
                 const size_t at = (size_t)(row0 + t) * pv.hq + (size_t)h * g + j;
                 const float2 st = P.stats[at];
-                float s = dot_key<D>(P.q_rot + at * D, d0, x, y);
-                if (P.alibi) s -= alibi_slope(h * g + j, pv.hq) * kLog2e * (float)(m - pos);
+                const float s = dot_key<D>(P.q_rot + at * D, d0, x, y);
                 if (see) sum += exp2f(s - st.x) * st.y;
             }
         }
@@ -289,7 +261,6 @@ Params make_params(const lazyattn_pool& p, const lazyattn_batch& b, const int32_
     Params P = {};
     P.entries = b.entries;
     P.entry_offsets = b.entry_offsets;
-    P.entry_delta = b.entry_delta;
     P.q_offsets = b.q_offsets;
     P.q_start = b.q_start;
     P.decode_qpos = decode_qpos;
@@ -298,29 +269,25 @@ Params make_params(const lazyattn_pool& p, const lazyattn_batch& b, const int32_
     P.window = window;
     P.sinks = sinks;
     P.causal = causal;
-    P.alibi = p.d.position_encoding == LAZYATTN_POS_ALIBI;
-    P.rotate_q = !P.alibi;
-    P.rotate_k = P.alibi || (b.flags & LAZYATTN_KEYS_PREROTATED) ? 0 : p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL ? 2 : 1;
+    P.rotate_k = !(b.flags & LAZYATTN_KEYS_PREROTATED);
     return P;
 }
 
-template <typename T>
 int launch_rows(const lazyattn_pool& p, const lazyattn_batch& b, const Params& P, const void* q, void* out,
                 cudaStream_t stream) {
     const int rows = P.decode_qpos ? 1 : b.max_q_len;
     if (rows < 1 || P.total_q < 1) return LAZYATTN_OK;
     const dim3 grid(rows, p.d.n_q_heads, b.num_requests);
-    auto k = p.d.head_dim == 64 ? rows_kernel<T, 64> : rows_kernel<T, 128>;
-    k<<<grid, kWarps * 32, 0, stream>>>(p.view(), P, static_cast<const T*>(q), static_cast<T*>(out));
+    auto k = p.d.head_dim == 64 ? rows_kernel<64> : rows_kernel<128>;
+    k<<<grid, kWarps * 32, 0, stream>>>(p.view(), P, static_cast<const float*>(q), static_cast<float*>(out));
     return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;
 }
 
-template <typename T>
 int launch_mass(const lazyattn_pool& p, const lazyattn_batch& b, const Params& P, const float* mass_in, float* mass_out,
                 float decay, cudaStream_t stream) {
     if (b.max_entries < 1) return LAZYATTN_OK;
     const dim3 grid((b.max_entries + kWarps - 1) / kWarps, p.d.n_kv_heads, b.num_requests);
-    auto k = p.d.head_dim == 64 ? mass_kernel<T, 64> : mass_kernel<T, 128>;
+    auto k = p.d.head_dim == 64 ? mass_kernel<64> : mass_kernel<128>;
     k<<<grid, kWarps * 32, 0, stream>>>(p.view(), P, mass_in, mass_out, decay);
     return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;
 }
@@ -330,7 +297,7 @@ int launch_mass(const lazyattn_pool& p, const lazyattn_batch& b, const Params& P
 int launch_window_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void* q, void* out,
                        const int32_t* decode_qpos, int32_t window, int32_t sinks, cudaStream_t stream) {
     const Params P = make_params(p, b, decode_qpos, window, sinks, true);
-    return launch_rows<float>(p, b, P, q, out, stream);
+    return launch_rows(p, b, P, q, out, stream);
 }
 
 size_t mass_simt_ws_bytes(const lazyattn_pool& p, int64_t rows) {
@@ -345,11 +312,8 @@ int launch_mass_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void
     P.stats = static_cast<float2*>(ws);
     P.q_rot = reinterpret_cast<float*>(static_cast<char*>(ws) +
                                        up256((size_t)P.total_q * (size_t)p.d.n_q_heads * sizeof(float2)));
-    const bool f32 = p.d.dtype == LAZYATTN_F32;
-    const int rc = f32 ? launch_rows<float>(p, b, P, q, out, stream) : launch_rows<__nv_bfloat16>(p, b, P, q, out, stream);
-    if (rc != LAZYATTN_OK) return rc;
-    return f32 ? launch_mass<float>(p, b, P, mass_in, mass_out, decay, stream)
-               : launch_mass<__nv_bfloat16>(p, b, P, mass_in, mass_out, decay, stream);
+    const int rc = launch_rows(p, b, P, q, out, stream);
+    return rc != LAZYATTN_OK ? rc : launch_mass(p, b, P, mass_in, mass_out, decay, stream);
 }
 
 }  // namespace lazyattn

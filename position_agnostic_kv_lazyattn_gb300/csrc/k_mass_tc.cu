@@ -1,0 +1,756 @@
+// Attention mass of a batch's query rows (bf16 pools) on tcgen05 / TMEM:
+//     mass[n] = sum over rows i of 2^(s_in - M_i) / L_i,   L_i = sum over n of 2^(s_in - M_i)
+// with s the scores in the log2 domain. L_i is not known before all of row i's
+// scores are, and keeping the scores (4 bytes each, against 0.75 ns of tensor time for 256
+// of them) would take more memory time than forming them again, so there are two passes over the
+// keys and a reduction:
+//   pass 1  S = Q K^T, thread = row: running maximum and sum per row
+//   pass 2  S^T = K Q^T (the same operands in shared memory, changed over), thread =
+//           key: the weights of its column summed in registers; one float per key and
+//           block of 128 rows goes to the workspace
+//   reduce  the row blocks' floats in order, plus decay * mass_in
+// No atomics: equal calls give equal bits.
+//
+// The scores are held to fp32 accuracy: a rotated q or k in one fp16 number would
+// be off by up to 2^-11, about 3e-4 on a weight. Each goes in as hi + lo (lo: the rounding of
+// the rest), and the accumulator takes K_lo Q_hi, K_hi Q_lo, then K_hi Q_hi, small
+// ones first. That is 24 MMAs of 128 x 128 x 16 per 128 x 128 scores, and what bounds both passes.
+//
+// CTA = (request, KV head, 128 rows = (token, head of the group) pairs, share of the
+// tiles of 128 keys). Roles (16 warps):
+//   warp 0        producer: block table, TMA of K pages and of their position-table rows
+//   warp 1        TMEM owner, MMA issuer
+//   warps 4-11    two warpgroups, taking the tiles in turn (two S buffers); each builds
+//                 half of the dims of Q first
+//   warps 12-15   rotation: thread = (page, 4 frequencies) over the page's 16 slots,
+//                 bf16 in place to hi, lo beside it
+// Two K stages of 64 KB (hi, lo), Q 64 KB. Every wait is bounded, as in the prefill kernel.
+#include <limits.h>
+
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace lazyattn {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kD = 128;
+constexpr int kTileM = 128;                        // rows per CTA
+constexpr int kN = 128;                            // keys per tile
+constexpr int kPagesPerTile = kN / kPage;          // 8
+constexpr int kStages = 2;
+constexpr int kInfoSlots = 4;
+constexpr int kThreads = 512;
+constexpr int kHalf = kTileM * 128;                // 16 KB: 64 dims of 128 rows or keys
+constexpr int kTile = 2 * kHalf;                   // 32 KB: one fp16 operand tile
+constexpr int kBaseBytes = kPagesPerTile * 512;    // 8 position-table rows
+constexpr int kOffQ = 0;                           // Q hi, Q lo
+constexpr int kOffK = kOffQ + 2 * kTile;           // stages of (K hi, K lo)
+constexpr int kOffBase = kOffK + kStages * 2 * kTile;
+constexpr int kSmemBytes = kOffBase + kStages * kBaseBytes + 1024;
+constexpr uint32_t kTmemCols = 256;                // two S buffers
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;          // log2 units
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+struct TileInfo {
+    int j;                        // tile index, -1: no more tiles
+    int start[kPagesPerTile];     // logical position of slot 0 of each page
+    int n[kPagesPerTile];         // keys in each page
+    int full_from;                // every page full: rows at positions >= this see every key; else INT_MAX
+};
+
+struct MassParams {
+    const uint64_t* entries;
+    const int32_t* entry_offsets;
+    const int32_t* entry_delta;   // doc-local pools
+    const int32_t* q_offsets;
+    const int32_t* q_start;
+    const __nv_bfloat16* q;
+    int32_t total_q, max_rows;    // max_rows: query tokens per request (host bound)
+    int32_t g;
+    int32_t oob_row;
+    int32_t row_blocks;           // rows of the position table's 16-row view
+    int32_t blocks;               // row blocks per request (host bound)
+    int32_t splits;
+    int32_t cap;                  // entries per request (host bound)
+    int32_t requests;
+    float2* stats;                // [r][h][block][split][warpgroup][128] (reference maximum, sum)
+    float* sums;                  // [block][r][cap][Hkv][16]
+};
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+// What the fp16 pair `hi` leaves of (a, b), rounded to fp16.
+__device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return pack_h2(a - f.x, b - f.y);
+}
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+    x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
+    x[4] = bf_lo(v.z); x[5] = bf_hi(v.z); x[6] = bf_lo(v.w); x[7] = bf_hi(v.w);
+}
+__device__ __forceinline__ void split8(const float (&x)[8], uint4& hi, uint4& lo) {
+    hi = make_uint4(pack_h2(x[0], x[1]), pack_h2(x[2], x[3]), pack_h2(x[4], x[5]), pack_h2(x[6], x[7]));
+    lo = make_uint4(rest_h2(x[0], x[1], hi.x), rest_h2(x[2], x[3], hi.y), rest_h2(x[4], x[5], hi.z),
+                    rest_h2(x[6], x[7], hi.w));
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Page in range and positions inside the table: number of keys, 0 if none, -1 if unusable.
+__device__ __forceinline__ int usable_tokens(const PoolView& pv, uint64_t e) {
+    const int n = entry_nvalid(e);
+    if (n == 0) return 0;
+    if (entry_page(e) >= (uint32_t)pv.num_pages || n > kPage || entry_start(e) + n > pv.max_position) return -1;
+    return n;
+}
+__device__ __forceinline__ int usable_local(const PoolView& pv, uint64_t e, int delta) {
+    const int n = usable_tokens(pv, e);
+    return n > 0 && (delta < 0 || delta > entry_start(e) || delta >= pv.max_position) ? -1 : n;
+}
+
+__device__ __forceinline__ size_t stats_at(const MassParams& P, int hkv, int r, int h, int block, int split, int wg) {
+    return ((((size_t)r * hkv + h) * P.blocks + block) * P.splits + split) * (2 * kTileM) + (size_t)wg * kTileM;
+}
+
+template <bool PREROT, bool LOCAL, bool INTER, bool ALIBI, int PASS>
+__global__ void __launch_bounds__(kThreads, 1)
+    mass_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kmap4,
+                   const __grid_constant__ CUtensorMap kmap8, const __grid_constant__ CUtensorMap rmap, PoolView pv,
+                   MassParams P) {
+    constexpr bool ROT = !PREROT && !ALIBI;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t bar_kfull[kStages], bar_kempty[kStages], bar_kready[kStages], bar_info[kInfoSlots];
+    __shared__ uint64_t bar_sfull[2], bar_sempty[2], bar_qready, bar_drain;
+    __shared__ TileInfo s_info[kInfoSlots];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ __align__(16) float2 s_row[PASS == 2 ? kTileM : 1];   // pass 2: (M, 1 / L) of each row
+
+    const int block = blockIdx.x / P.splits, split = blockIdx.x - block * P.splits;
+    const int h = blockIdx.y, r = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = P.g, Hq = pv.hq, Hkv = pv.hkv;
+    const int TQ = kTileM / g;
+    const int q0 = P.q_offsets[r], q1 = P.q_offsets[r + 1];
+    const int i0 = block * TQ;
+    const int tokens = min(q1 - q0, P.max_rows);
+    if (i0 >= tokens) return;
+    if (q1 > P.total_q) {
+        if (threadIdx.x == 0) record_error(pv.status, LAZYATTN_ERANGE);
+        return;
+    }
+    const int ntok = min(TQ, tokens - i0);
+    const int m_lo = P.q_start[r] + i0, m_hi = m_lo + ntok - 1;
+    const int e0 = P.entry_offsets[r], e1 = min(P.entry_offsets[r + 1], e0 + P.cap);
+    const int t_all = e1 > e0 ? (e1 - e0 + kPagesPerTile - 1) / kPagesPerTile : 0;
+    const int chunk = (t_all + P.splits - 1) / P.splits;
+    const int jb = min(t_all, split * chunk), T = min(t_all, jb + chunk) - jb;
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&bar_kfull[s]), 1);
+            mbar_init(smem_u32(&bar_kempty[s]), 1);
+            mbar_init(smem_u32(&bar_kready[s]), 4);
+        }
+        for (int s = 0; s < kInfoSlots; ++s) mbar_init(smem_u32(&bar_info[s]), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar_sfull[i]), 1);
+            mbar_init(smem_u32(&bar_sempty[i]), 4);
+        }
+        mbar_init(smem_u32(&bar_qready), 8);
+        mbar_init(smem_u32(&bar_drain), 1);
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* abort_flag = &s_abort;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        // A K stage is free once the MMAs that read it are done; that also frees the
+        // info slot of the tile before: its scores were read before those MMAs were issued.
+        // Two sentinels end the stream, one for each warpgroup that takes tiles in turn.
+        if (lane == 0) {
+            auto load_entries = [&](int jj, uint64_t (&e)[kPagesPerTile], int (&dl)[kPagesPerTile]) {
+#pragma unroll
+                for (int p = 0; p < kPagesPerTile; ++p) {
+                    const int idx = e0 + (jb + jj) * kPagesPerTile + p;
+                    const uint64_t v = P.entries[min(idx, e1 - 1)];
+                    e[p] = idx < e1 ? v : 0ull;
+                    if (LOCAL) dl[p] = P.entry_delta[min(idx, e1 - 1)];
+                }
+            };
+            int last_k[kStages];
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) last_k[s] = -1;
+            uint64_t cur[kPagesPerTile] = {}, nxt[kPagesPerTile] = {};
+            int curd[kPagesPerTile] = {}, nxtd[kPagesPerTile] = {};
+            if (T > 0) load_entries(0, cur, curd);
+            int k = 0;
+            bool ok = true;
+            for (int j = 0; ok && j < T; ++j) {
+                if (j + 1 < T) load_entries(j + 1, nxt, nxtd);
+                int n[kPagesPerTile], ys[kPagesPerTile], ss[kPagesPerTile];
+                bool live = false, bad = false;
+                int consec = 3, full_from = 0;
+#pragma unroll
+                for (int p = 0; p < kPagesPerTile; ++p) {
+                    n[p] = LOCAL ? usable_local(pv, cur[p], curd[p]) : usable_tokens(pv, cur[p]);
+                    bad = bad || n[p] < 0;
+                    n[p] = max(n[p], 0);
+                    ss[p] = entry_start(cur[p]);
+                    live = live || (n[p] > 0 && ss[p] <= m_hi);
+                    ys[p] = n[p] > 0 ? ((int)entry_page(cur[p]) * Hkv + h) * kPage : P.oob_row;
+                    if (n[p] == 0 || entry_page(cur[p]) != entry_page(cur[p & ~3]) + (uint32_t)(p & 3))
+                        consec &= ~(1 << (p >> 2));
+                    full_from = n[p] == kPage ? max(full_from, ss[p] + kPage - 1) : INT_MAX;
+                }
+                if (bad) record_error(pv.status, LAZYATTN_ERANGE);
+                if (live) {
+                    const int st = k % kStages;
+                    const int pg0 = (int)entry_page(cur[0]), pg1 = (int)entry_page(cur[4]);
+                    if (consec == 3 && pg1 == pg0 + 4) consec |= 4;
+                    const int t0 = ss[0];
+                    bool strided = ROT && !LOCAL && P.row_blocks > 0 && t0 / kPage + kPagesPerTile <= P.row_blocks;
+#pragma unroll
+                    for (int p = 0; p < kPagesPerTile; ++p) strided = strided && n[p] > 0 && ss[p] == t0 + kPage * p;
+                    ok = k < kStages || mbar_wait(smem_u32(&bar_kempty[st]), ((k / kStages) - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const uint32_t fb = smem_u32(&bar_kfull[st]);
+                    const uint32_t ds = smem_u32(sm + kOffK + st * 2 * kTile);
+                    const uint32_t bs = smem_u32(sm + kOffBase + st * kBaseBytes);
+                    mbar_expect_tx(fb, kTile + (ROT ? kBaseBytes : 0));
+                    if (consec & 4) {
+                        tma_load_4d(ds, &kmap8, 0, 0, h, pg0, fb);
+                        tma_load_4d(ds + kHalf, &kmap8, 64, 0, h, pg0, fb);
+                    } else {
+#pragma unroll
+                        for (int b4 = 0; b4 < 2; ++b4) {
+                            if (consec & (1 << b4)) {
+                                const int pg = b4 ? pg1 : pg0;
+                                tma_load_4d(ds + b4 * 8192, &kmap4, 0, 0, h, pg, fb);
+                                tma_load_4d(ds + kHalf + b4 * 8192, &kmap4, 64, 0, h, pg, fb);
+                            } else {
+#pragma unroll
+                                for (int p = 4 * b4; p < 4 * b4 + 4; ++p) {
+                                    tma_load_2d(ds + p * 2048, &kmap, 0, ys[p], fb);
+                                    tma_load_2d(ds + kHalf + p * 2048, &kmap, 64, ys[p], fb);
+                                }
+                            }
+                        }
+                    }
+                    if (strided) {
+                        tma_load_3d(bs, &rmap, 0, t0 % kPage, t0 / kPage, fb);
+                    } else if (ROT) {
+#pragma unroll
+                        for (int p = 0; p < kPagesPerTile; ++p) {
+                            const int rowpos = LOCAL ? curd[p] : ss[p];
+                            bulk_load(bs + p * 512, pv.rope_pair + (n[p] > 0 ? (size_t)rowpos * (kD / 4) : 0), 512, fb);
+                        }
+                    }
+                    TileInfo& info = s_info[k & (kInfoSlots - 1)];
+                    info.j = jb + j;
+                    info.full_from = full_from;
+#pragma unroll
+                    for (int p = 0; p < kPagesPerTile; ++p) {
+                        info.start[p] = ss[p];
+                        info.n[p] = n[p];
+                    }
+                    mbar_arrive(smem_u32(&bar_info[k & (kInfoSlots - 1)]));
+                    mbar_arrive(fb);
+                    last_k[st] = k;
+                    ++k;
+                }
+#pragma unroll
+                for (int p = 0; p < kPagesPerTile; ++p) {
+                    cur[p] = nxt[p];
+                    curd[p] = nxtd[p];
+                }
+            }
+            for (int i = 0; ok && i < 2; ++i, ++k) {
+                const int st = k % kStages;
+                ok = k < kStages || mbar_wait(smem_u32(&bar_kempty[st]), ((k / kStages) - 1) & 1, abort_flag);
+                if (!ok) break;
+                s_info[k & (kInfoSlots - 1)].j = -1;
+                mbar_arrive(smem_u32(&bar_info[k & (kInfoSlots - 1)]));
+                if (i == 0) mbar_arrive(smem_u32(&bar_kfull[st]));
+            }
+            if (!ok) *abort_flag = 1;
+            if (*abort_flag) {   // issued copies land before the CTA's shared memory is released
+                volatile int never = 0;
+                for (int s = 0; s < kStages; ++s)
+                    if (last_k[s] >= 0) mbar_wait(smem_u32(&bar_kfull[s]), (last_k[s] / kStages) & 1, &never);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t id = idesc_f16(kTileM, kN, 0, 0, 0);
+            const uint64_t dq = sdesc_sw128(smem_u32(sm + kOffQ), 16, 1024);
+            const uint64_t dk = sdesc_sw128(smem_u32(sm + kOffK), 16, 1024);
+            bool ok = mbar_wait(smem_u32(&bar_qready), 0, abort_flag);
+            for (int k = 0; ok; ++k) {
+                const int st = k % kStages, ph = (k / kStages) & 1, b = k & 1;
+                ok = mbar_wait(smem_u32(&bar_kready[st]), ph, abort_flag);
+                if (!ok || s_info[k & (kInfoSlots - 1)].j < 0) break;
+                ok = k < 2 || mbar_wait(smem_u32(&bar_sempty[b]), ((k >> 1) - 1) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ks = dk + (uint64_t)(st * (2 * kTile >> 4));
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {   // K_lo Q_hi, K_hi Q_lo, K_hi Q_hi
+                    const uint64_t ka = ks + (part == 0 ? (uint64_t)(kTile >> 4) : 0);
+                    const uint64_t qa = dq + (part == 1 ? (uint64_t)(kTile >> 4) : 0);
+#pragma unroll
+                    for (int t = 0; t < kD / 16; ++t) {
+                        const uint64_t o = (uint64_t)(((t >> 2) * kHalf + (t & 3) * 32) >> 4);
+                        umma_f16(tmem + b * 128, (PASS == 1 ? qa : ka) + o, (PASS == 1 ? ka : qa) + o, id,
+                                 part > 0 || t > 0 ? 1u : 0u);
+                    }
+                }
+                umma_commit(smem_u32(&bar_sfull[b]));
+                umma_commit(smem_u32(&bar_kempty[st]));
+            }
+            umma_commit(smem_u32(&bar_drain));
+            volatile int never = 0;
+            mbar_wait(smem_u32(&bar_drain), 0, &never);
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------ K rotation
+        const int rt = threadIdx.x - 384;
+        const int p = rt >> 4, u = rt & 15;
+        float c1[4], s1[4];   // theta of frequencies 4u .. 4u + 3
+        if (ROT && !LOCAL) {
+            const float4* t4 = pv.rope_pair + (size_t)(kD / 4) + 2 * u;   // position 1
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float4 f = pv.max_position > 1 ? __ldg(t4 + v) : make_float4(1.f, 1.f, 0.f, 0.f);
+                c1[2 * v] = f.x; c1[2 * v + 1] = f.y;
+                s1[2 * v] = f.z; s1[2 * v + 1] = f.w;
+            }
+        }
+        auto rot_wait = [&](uint32_t bar, uint32_t parity) {   // one poller; the same answer for all 128 threads
+            int go = 1;
+            if (rt == 0) go = mbar_wait(bar, parity, abort_flag) ? 1 : 0;
+            go = go && *abort_flag == 0;
+            int all;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
+                "selp.b32 %0, 1, 0, q;\n\t}"
+                : "=r"(all)
+                : "r"(go)
+                : "memory");
+            return all != 0;
+        };
+        for (int k = 0;; ++k) {
+            const int st = k % kStages, ph = (k / kStages) & 1;
+            if (!rot_wait(smem_u32(&bar_kfull[st]), ph)) break;
+            const TileInfo& info = s_info[k & (kInfoSlots - 1)];
+            if (info.j < 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_kready[st]));
+                break;
+            }
+            const int np = info.n[p];
+            uint8_t* kb = sm + kOffK + st * 2 * kTile + (2 * p) * 1024 + (u & 1) * 8;
+            float C[4], S[4];
+            if (ROT) {
+                const float4* b4 = reinterpret_cast<const float4*>(sm + kOffBase + st * kBaseBytes + p * 512) + 2 * u;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const float4 b = b4[v];
+                    C[2 * v] = b.x; C[2 * v + 1] = b.y;
+                    S[2 * v] = b.z; S[2 * v + 1] = b.w;
+                }
+            }
+#pragma unroll 1
+            for (int s8 = 0; s8 < 2; ++s8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint2* p1 = reinterpret_cast<uint2*>(kb + s8 * 1024 + j * 128 + (((u >> 1) ^ j) << 4));
+                    uint2* p2 = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p1) + kHalf);
+                    uint2 h1 = make_uint2(0, 0), h2 = h1, l1 = h1, l2 = h1;
+                    if (8 * s8 + j < np) {
+                        const uint2 a = *p1, z = *p2;
+                        float x[4] = {bf_lo(a.x), bf_hi(a.x), bf_lo(a.y), bf_hi(a.y)};
+                        float y[4] = {bf_lo(z.x), bf_hi(z.x), bf_lo(z.y), bf_hi(z.y)};
+                        if (ROT) {
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                const float f = x[v] * C[v] - y[v] * S[v];
+                                y[v] = x[v] * S[v] + y[v] * C[v];
+                                x[v] = f;
+                            }
+                        }
+                        h1 = make_uint2(pack_h2(x[0], x[1]), pack_h2(x[2], x[3]));
+                        h2 = make_uint2(pack_h2(y[0], y[1]), pack_h2(y[2], y[3]));
+                        l1 = make_uint2(rest_h2(x[0], x[1], h1.x), rest_h2(x[2], x[3], h1.y));
+                        l2 = make_uint2(rest_h2(y[0], y[1], h2.x), rest_h2(y[2], y[3], h2.y));
+                    }
+                    *p1 = h1;
+                    *p2 = h2;
+                    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p1) + kTile) = l1;
+                    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p2) + kTile) = l2;
+                    if (ROT && !LOCAL) {   // next slot: angle + theta
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const float cc = C[v] * c1[v] - S[v] * s1[v];
+                            S[v] = S[v] * c1[v] + C[v] * s1[v];
+                            C[v] = cc;
+                        }
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_kready[st]));
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ rows / keys
+        const int wg = (warp - 4) >> 2, quarter = warp & 3;
+        const int trow = 32 * quarter + lane;      // row of Q (pass 1), key of the tile (pass 2): TMEM lane
+        const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16) + wg * 128;
+        const int t_local = trow / g, jh = trow - t_local * g;
+        const int m_row = m_lo + t_local;
+        bool row_valid = t_local < ntok;
+        if (row_valid && (m_row < 0 || m_row >= pv.max_position)) {
+            record_error(pv.status, LAZYATTN_ERANGE);
+            row_valid = false;
+        }
+        {   // Q: this warpgroup's 32 dims of each half of its row, rotated at m_row and scaled, hi and lo
+            uint8_t* qsm = sm + kOffQ;
+            const float sc = kLog2e * pv.qk_scale;
+            const __nv_bfloat16* qp = P.q + ((size_t)(q0 + i0 + t_local) * Hq + (size_t)h * g + jh) * kD;
+            const float* cs = reinterpret_cast<const float*>(pv.rope + (size_t)(row_valid ? m_row : 0) * (kD / 2));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int u = 4 * wg + i;
+                uint4 h1 = make_uint4(0, 0, 0, 0), h2 = h1, l1 = h1, l2 = h1;
+                if (row_valid) {
+                    uint4 a = __ldg(reinterpret_cast<const uint4*>(qp + (INTER ? 16 * u : 8 * u)));
+                    uint4 b = __ldg(reinterpret_cast<const uint4*>(qp + (INTER ? 16 * u + 8 : 64 + 8 * u)));
+                    if (INTER) deinterleave16(a, b, a, b);
+                    float x1[8], x2[8], n2 = 0.f;
+                    unpack8(a, x1);
+                    unpack8(b, x2);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) n2 = fmaxf(n2, fmaf(x1[v], x1[v], x2[v] * x2[v]));
+                    if (!(n2 * sc * sc <= kMaxPairNorm2)) record_error(pv.status, LAZYATTN_ERANGE);
+                    const float4* c4 = reinterpret_cast<const float4*>(cs + 16 * u);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const float4 f = ALIBI ? make_float4(1.f, 0.f, 1.f, 0.f) : __ldg(c4 + v);
+                        const float a0 = x1[2 * v], z0 = x2[2 * v], a1 = x1[2 * v + 1], z1 = x2[2 * v + 1];
+                        x1[2 * v] = (a0 * f.x - z0 * f.y) * sc;
+                        x2[2 * v] = (a0 * f.y + z0 * f.x) * sc;
+                        x1[2 * v + 1] = (a1 * f.z - z1 * f.w) * sc;
+                        x2[2 * v + 1] = (a1 * f.w + z1 * f.z) * sc;
+                    }
+                    split8(x1, h1, l1);
+                    split8(x2, h2, l2);
+                }
+                const uint32_t o = sw128_offset(trow, u);
+                *reinterpret_cast<uint4*>(qsm + o) = h1;
+                *reinterpret_cast<uint4*>(qsm + kHalf + o) = h2;
+                *reinterpret_cast<uint4*>(qsm + kTile + o) = l1;
+                *reinterpret_cast<uint4*>(qsm + kTile + kHalf + o) = l2;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_qready));
+        }
+        if (PASS == 2) {   // merge the rows' statistics: warpgroup 0, one row a thread
+            grid_dep_wait();
+            if (wg == 0) {
+                float M = -INFINITY, Lsum = 0.f;
+                for (int i = 0; i < 2 * P.splits; ++i) {
+                    const float2 x = P.stats[stats_at(P, Hkv, r, h, block, i >> 1, i & 1) + trow];
+                    if (x.y > 0.f) M = fmaxf(M, x.x);
+                }
+                for (int i = 0; i < 2 * P.splits && M != -INFINITY; ++i) {
+                    const float2 x = P.stats[stats_at(P, Hkv, r, h, block, i >> 1, i & 1) + trow];
+                    if (x.y > 0.f) Lsum += x.y * fast_exp2(x.x - M);
+                }
+                s_row[trow] = Lsum > 0.f ? make_float2(M, 1.f / Lsum) : make_float2(0.f, 0.f);
+            }
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+        }
+
+        float m_run = -INFINITY, l_run = 0.f;
+        bool ok = true;
+        for (int k = wg;; k += 2) {
+            const int is = k & (kInfoSlots - 1);
+            ok = mbar_wait(smem_u32(&bar_info[is]), (k / kInfoSlots) & 1, abort_flag);
+            if (!ok) break;
+            const TileInfo& info = s_info[is];
+            const int j = info.j;
+            if (j < 0) break;
+            if (PASS == 1) {
+                const float slope = ALIBI ? alibi_slope(h * g + jh, Hq) * kLog2e : 0.f;
+                const bool wfull = __all_sync(0xffffffffu, row_valid && m_row >= info.full_from);
+                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+#pragma unroll
+                for (int w = 0; w < 4 && !wfull; ++w) {
+                    uint32_t bits = 0;
+#pragma unroll
+                    for (int hp = 0; hp < 2; ++hp) {
+                        const int p = 2 * w + hp;
+                        const int l = row_valid ? max(min(info.n[p], m_row - info.start[p] + 1), 0) : 0;
+                        bits |= ((1u << l) - 1u) << (16 * hp);
+                    }
+                    vis[w] = bits;
+                }
+                int dist[kPagesPerTile];   // ALiBi: position of each page's slot 0 relative to the row
+#pragma unroll
+                for (int p = 0; p < kPagesPerTile; ++p) dist[p] = ALIBI ? info.start[p] - m_row : 0;
+                ok = mbar_wait(smem_u32(&bar_sfull[wg]), (k >> 1) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t v[64];
+                    tmem_ld64(tl + 64 * hh, v);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (ALIBI) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            v[i] = __float_as_uint(__uint_as_float(v[i]) +
+                                                   slope * (float)(dist[4 * hh + (i >> 4)] + (i & 15)));
+                    }
+                    if (!wfull) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            v[i] = (vis[2 * hh + (i >> 5)] >> (i & 31)) & 1u ? v[i] : 0xff800000u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        mx[i & 3] = fmax3(mx[i & 3], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (top > m_run + kRescaleThreshold) {
+                        l_run *= fast_exp2(m_run - top);   // 0 while m_run is -inf
+                        m_run = top;
+                    }
+                    const float ref = m_run == -INFINITY ? 0.f : m_run;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) sum[i & 3] += fast_exp2(__uint_as_float(v[i]) - ref);
+                    l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_sempty[wg]));
+            } else {
+                // key trow: columns c >= c0 hold the rows that see it (positions go up with the row)
+                const int p = trow >> 4, slot = trow & 15;
+                const int pos = info.start[p] + slot;
+                const int64_t before = (int64_t)pos - m_lo;
+                const int c0 = slot < info.n[p] ? (int)min((int64_t)kTileM, max((int64_t)0, before * g)) : kTileM;
+                ok = mbar_wait(smem_u32(&bar_sfull[wg]), (k >> 1) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const bool wfull = __all_sync(0xffffffffu, c0 == 0);
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t v[64];
+                    tmem_ld64(tl + 64 * hh, v);
+                    if (ALIBI) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) {
+                            const int c = 64 * hh + i, t = c / g;
+                            v[i] = __float_as_uint(__uint_as_float(v[i]) + alibi_slope(h * g + c - t * g, Hq) * kLog2e *
+                                                                                (float)(pos - (m_lo + t)));
+                        }
+                    }
+                    if (!wfull) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) v[i] = 64 * hh + i >= c0 ? v[i] : 0xff800000u;
+                    }
+                    const float4* rows = reinterpret_cast<const float4*>(s_row) + 32 * hh;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float4 st = rows[i];   // (M, 1 / L) of columns 2i, 2i + 1
+                        sum[2 * (i & 1)] += fast_exp2(__uint_as_float(v[2 * i]) - st.x) * st.y;
+                        sum[2 * (i & 1) + 1] += fast_exp2(__uint_as_float(v[2 * i + 1]) - st.z) * st.w;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_sempty[wg]));
+                const int idx = j * kPagesPerTile + p;
+                if (idx < e1 - e0)
+                    P.sums[((((size_t)block * P.requests + r) * P.cap + idx) * Hkv + h) * kPage + slot] =
+                        (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            }
+        }
+        if (PASS == 1)
+            P.stats[stats_at(P, Hkv, r, h, block, split, wg) + trow] =
+                make_float2(m_run == -INFINITY ? 0.f : m_run, ok && row_valid ? l_run : 0.f);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && s_abort) record_error(pv.status, LAZYATTN_EDEVICE);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Thread = (entry, KV head, slot): the row blocks' sums in order. A block has written an
+// entry's sums iff the entry starts at or before the block's last row.
+template <bool LOCAL>
+__global__ void __launch_bounds__(256)
+    mass_reduce_kernel(PoolView pv, MassParams P, const float* mass_in, float* mass_out, float decay) {
+    const int r = blockIdx.y;
+    const int per = pv.hkv * kPage;
+    grid_dep_wait();
+    const int e0 = P.entry_offsets[r], E = P.entry_offsets[r + 1] - e0;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int i = (int)(at / per), rest = (int)(at - (int64_t)i * per);
+    if (i >= min(E, P.cap)) return;
+    const uint64_t e = P.entries[e0 + i];
+    const int n = LOCAL ? usable_local(pv, e, P.entry_delta[e0 + i]) : usable_tokens(pv, e);
+    const size_t to = (size_t)(e0 + i) * per + rest;
+    float sum = 0.f;
+    if ((rest & 15) < n) {
+        const int q0 = P.q_offsets[r], q1 = P.q_offsets[r + 1];
+        const int tokens = q1 <= P.total_q ? min(q1 - q0, P.max_rows) : 0;
+        const int TQ = kTileM / P.g, m0 = P.q_start[r];
+        for (int b = 0; b * TQ < tokens; ++b)
+            if (entry_start(e) <= m0 + min((b + 1) * TQ, tokens) - 1)
+                sum += P.sums[(((size_t)b * P.requests + r) * P.cap + i) * per + rest];
+        if (mass_in) sum += decay * mass_in[to];
+    }
+    mass_out[to] = sum;
+}
+
+using MassKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, PoolView,
+                            MassParams);
+
+template <int PASS>
+MassKernel mass_kernel_for(bool prerot, bool local, bool inter, bool alibi) {
+    if (alibi) return mass_tc_kernel<false, false, false, true, PASS>;
+    if (local) return inter ? mass_tc_kernel<false, true, true, false, PASS> : mass_tc_kernel<false, true, false, false, PASS>;
+    if (prerot) return inter ? mass_tc_kernel<true, false, true, false, PASS> : mass_tc_kernel<true, false, false, false, PASS>;
+    return inter ? mass_tc_kernel<false, false, true, false, PASS> : mass_tc_kernel<false, false, false, false, PASS>;
+}
+
+inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct MassWs {
+    int blocks, splits;
+    size_t sums_off, total;
+};
+
+// CTAs per (request, KV head, row block): the split with the least time by waves of
+// CTAs, each its tiles plus a start and an end of about four tiles' time; shares of 4 tiles or more.
+MassWs mass_ws(const lazyattn_pool& p, const lazyattn_batch& b) {
+    MassWs w;
+    const int g = p.d.n_q_heads / p.d.n_kv_heads, TQ = kTileM / g;
+    w.blocks = std::max(1, (b.max_q_len + TQ - 1) / TQ);
+    const int64_t items = (int64_t)b.num_requests * p.d.n_kv_heads * w.blocks;
+    const int64_t T = ((int64_t)b.max_entries + kPagesPerTile - 1) / kPagesPerTile;
+    const int64_t sms = p.sm_count > 0 ? p.sm_count : 1;
+    w.splits = 1;
+    double best = 0.0;
+    for (int s = 1; s <= 16; ++s) {
+        if (s > 1 && T / s < 4) break;
+        const double cost = (double)((items * s + sms - 1) / sms) * ((double)((T + s - 1) / s) + 4.0);
+        if (s == 1 || cost < best) {
+            best = cost;
+            w.splits = s;
+        }
+    }
+    w.sums_off = up256((size_t)items * w.splits * 2 * kTileM * sizeof(float2));
+    w.total = w.sums_off + up256((size_t)w.blocks * b.num_requests * (size_t)std::max(b.max_entries, 1) *
+                                 p.d.n_kv_heads * kPage * sizeof(float));
+    return w;
+}
+
+}  // namespace
+
+int mass_tc_init() {
+    for (int i = 0; i < 9; ++i) {
+        if (i < 8 && (i & 1) && (i & 2)) continue;   // pre-rotated pages are never doc-local
+        const bool alibi = i == 8;
+        MassKernel k1 = mass_kernel_for<1>(!alibi && (i & 1), !alibi && (i & 2), !alibi && (i & 4), alibi);
+        MassKernel k2 = mass_kernel_for<2>(!alibi && (i & 1), !alibi && (i & 2), !alibi && (i & 4), alibi);
+        if (cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+            return LAZYATTN_ECUDA;
+    }
+    return LAZYATTN_OK;
+}
+
+size_t mass_tc_ws_bytes(const lazyattn_pool& p, const lazyattn_batch& b) { return mass_ws(p, b).total; }
+
+int launch_prefill_mass_bf16(const lazyattn_pool& p, const lazyattn_batch& b, const __nv_bfloat16* q,
+                             const float* mass_in, float* mass_out, float decay, void* ws, cudaStream_t stream) {
+    if (!p.have_maps) return LAZYATTN_ECUDA;
+    if (b.max_entries < 1) return LAZYATTN_OK;
+    const MassWs w = mass_ws(p, b);
+    MassParams P;
+    P.entries = b.entries;
+    P.entry_offsets = b.entry_offsets;
+    P.entry_delta = b.entry_delta;
+    P.q_offsets = b.q_offsets;
+    P.q_start = b.q_start;
+    P.q = q;
+    P.total_q = b.total_q;
+    P.max_rows = b.max_q_len;
+    P.g = p.d.n_q_heads / p.d.n_kv_heads;
+    P.oob_row = (int32_t)((uint64_t)p.d.num_pages * (uint64_t)p.d.n_kv_heads * kPage);
+    P.row_blocks = p.have_rmap ? p.d.max_position / kPage : 0;
+    P.blocks = w.blocks;
+    P.splits = w.splits;
+    P.cap = b.max_entries;
+    P.requests = b.num_requests;
+    P.stats = static_cast<float2*>(ws);
+    P.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + w.sums_off);
+    const bool prerot = (b.flags & LAZYATTN_KEYS_PREROTATED) != 0, inter = p.d.rope_interleaved != 0;
+    const bool local = p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL, alibi = p.d.position_encoding == LAZYATTN_POS_ALIBI;
+    if (b.total_q > 0 && b.max_q_len > 0) {
+        const dim3 grid(w.blocks * w.splits, p.d.n_kv_heads, b.num_requests);
+        mass_kernel_for<1>(prerot, local, inter, alibi)<<<grid, kThreads, kSmemBytes, stream>>>(p.kmap, p.kmap4, p.kmap8,
+                                                                                                p.rmap, p.view(), P);
+        if (cudaGetLastError() != cudaSuccess ||
+            launch_dependent(mass_kernel_for<2>(prerot, local, inter, alibi), grid, dim3(kThreads), kSmemBytes, stream,
+                             p.kmap, p.kmap4, p.kmap8, p.rmap, p.view(), P) != cudaSuccess)
+            return LAZYATTN_ECUDA;
+    } else {
+        P.max_rows = 0;
+    }
+    const int64_t threads = (int64_t)b.max_entries * p.d.n_kv_heads * kPage;
+    if (launch_dependent(local ? mass_reduce_kernel<true> : mass_reduce_kernel<false>,
+                         dim3((unsigned)((threads + 255) / 256), b.num_requests), dim3(256), 0, stream, p.view(), P, mass_in,
+                         mass_out, decay) != cudaSuccess)
+        return LAZYATTN_ECUDA;
+    return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;
+}
+
+}  // namespace lazyattn

@@ -167,7 +167,7 @@ int lazyattn_pool_create(const lazyattn_pool_desc* desc, void* stream, lazyattn_
     }
     int occ = 1;
     if (d.dtype == LAZYATTN_BF16 && (decode_occupancy(&occ) != LAZYATTN_OK || prefill_init() != LAZYATTN_OK ||
-                                     decode_shared_init() != LAZYATTN_OK)) {
+                                     decode_shared_init() != LAZYATTN_OK || mass_tc_init() != LAZYATTN_OK)) {
         delete p;
         return LAZYATTN_ECUDA;
     }
@@ -366,6 +366,7 @@ size_t lazyattn_workspace_size(lazyattn_pool_t pool, int32_t op, const lazyattn_
     if (op == LAZYATTN_OP_PREFILL) {
         return prefill_bytes(pool, batch, INT32_MAX, 0);
     }
+    if (op == LAZYATTN_OP_PREFILL_MASS && pool->d.dtype == LAZYATTN_BF16) return mass_tc_ws_bytes(*pool, *batch);
     if (op == LAZYATTN_OP_PREFILL_MASS) return mass_simt_ws_bytes(*pool, batch->total_q) + 256;
     if (op == LAZYATTN_OP_DECODE_MASS && pool->d.dtype == LAZYATTN_BF16) return decode_mass_ws_layout(*pool, *batch).total;
     if (op == LAZYATTN_OP_DECODE_MASS) return qpos_bytes(batch) + mass_simt_ws_bytes(*pool, batch->num_requests);
@@ -487,8 +488,11 @@ int lazyattn_prefill_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, con
     if (workspace_bytes < lazyattn_workspace_size(pool, LAZYATTN_OP_PREFILL_MASS, batch)) return LAZYATTN_EWORKSPACE;
     rc = check_device(pool);
     if (rc != LAZYATTN_OK) return rc;
-    return launch_mass_simt(*pool, *batch, q, nullptr, nullptr, mass_in, mass_out, decay, workspace,
-                            static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pool->d.dtype == LAZYATTN_BF16)
+        return launch_prefill_mass_bf16(*pool, *batch, static_cast<const __nv_bfloat16*>(q), mass_in, mass_out, decay,
+                                        workspace, st);
+    return launch_mass_simt(*pool, *batch, q, nullptr, nullptr, mass_in, mass_out, decay, workspace, st);
 }
 
 int lazyattn_decode_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const void* k_new,
