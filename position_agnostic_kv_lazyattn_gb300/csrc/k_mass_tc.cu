@@ -17,13 +17,13 @@
 // ones first. That is 24 MMAs of 128 x 128 x 16 per 128 x 128 scores, and what bounds both passes.
 //
 // CTA = (request, KV head, 128 rows = (token, head of the group) pairs, share of the
-// tiles of 128 keys). Roles (16 warps):
+// tiles of 128 keys). Roles (20 warps):
 //   warp 0        producer: block table, TMA of K pages and of their position-table rows
 //   warp 1        TMEM owner, MMA issuer
 //   warps 4-11    two warpgroups, taking the tiles in turn (two S buffers); each builds
 //                 half of the dims of Q first
-//   warps 12-15   rotation: thread = (page, 4 frequencies) over the page's 16 slots,
-//                 bf16 in place to hi, lo beside it
+//   warps 12-19   rotation: thread = (page, half of its slots, 4 frequencies), bf16 in
+//                 place to hi, lo beside it
 // Two K stages of 64 KB (hi, lo), Q 64 KB. Every wait is bounded, as in the prefill kernel.
 #include <limits.h>
 
@@ -42,7 +42,7 @@ constexpr int kN = 128;                            // keys per tile
 constexpr int kPagesPerTile = kN / kPage;          // 8
 constexpr int kStages = 2;
 constexpr int kInfoSlots = 4;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kHalf = kTileM * 128;                // 16 KB: 64 dims of 128 rows or keys
 constexpr int kTile = 2 * kHalf;                   // 32 KB: one fp16 operand tile
 constexpr int kBaseBytes = kPagesPerTile * 512;    // 8 position-table rows
@@ -85,10 +85,41 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
 }
+// Two fp32 lanes per instruction (packed f32x2 arithmetic).
+__device__ __forceinline__ uint64_t pack2(float2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t r) {
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+__device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 f2_sub(float2 a, float2 b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
+    return unpack2(r);
+}
 // What the fp16 pair `hi` leaves of (a, b), rounded to fp16.
 __device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t hi) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    return pack_h2(a - f.x, b - f.y);
+    const float2 f = f2_sub(make_float2(a, b), __half22float2(*reinterpret_cast<const __half2*>(&hi)));
+    return pack_h2(f.x, f.y);
 }
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
@@ -141,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ TileInfo s_info[kInfoSlots];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ __align__(16) float2 s_row[PASS == 2 ? kTileM : 1];   // pass 2: (M, 1 / L) of each row
+    __shared__ __align__(16) float s_row[PASS == 2 ? 2 * kTileM : 4];   // pass 2: (-M, -M, 1 / L, 1 / L) of rows 2i, 2i + 1
 
     const int block = blockIdx.x / P.splits, split = blockIdx.x - block * P.splits;
     const int h = blockIdx.y, r = blockIdx.z;
@@ -168,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&bar_kfull[s]), 1);
             mbar_init(smem_u32(&bar_kempty[s]), 1);
-            mbar_init(smem_u32(&bar_kready[s]), 4);
+            mbar_init(smem_u32(&bar_kready[s]), 8);
         }
         for (int s = 0; s < kInfoSlots; ++s) mbar_init(smem_u32(&bar_info[s]), 1);
         for (int i = 0; i < 2; ++i) {
@@ -341,25 +372,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 12) {
         // ------------------------------------------------------------ K rotation
+        // Thread = (page p, half s8 of its slots, frequencies 4u .. 4u + 3). The angle of
+        // slot 0 is the page's row of the position table; slot 8's is that plus 8 theta; each
+        // next one turns by theta (angle addition, two frequencies an instruction).
         const int rt = threadIdx.x - 384;
-        const int p = rt >> 4, u = rt & 15;
-        float c1[4], s1[4];   // theta of frequencies 4u .. 4u + 3
+        const int p = rt >> 5, s8 = (rt >> 4) & 1, u = rt & 15;
+        float2 c1[2], s1[2], ns1[2], c8[2], z8[2];
         if (ROT && !LOCAL) {
-            const float4* t4 = pv.rope_pair + (size_t)(kD / 4) + 2 * u;   // position 1
+            auto row = [&](int pos, int v) {   // the paired table's (cos, cos, sin, sin); positions past it: no key there
+                return pos < pv.max_position ? __ldg(pv.rope_pair + (size_t)pos * (kD / 4) + 2 * u + v)
+                                             : make_float4(1.f, 1.f, 0.f, 0.f);
+            };
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
-                const float4 f = pv.max_position > 1 ? __ldg(t4 + v) : make_float4(1.f, 1.f, 0.f, 0.f);
-                c1[2 * v] = f.x; c1[2 * v + 1] = f.y;
-                s1[2 * v] = f.z; s1[2 * v + 1] = f.w;
+                const float4 f = row(1, v), e = row(8 * s8, v);
+                c1[v] = make_float2(f.x, f.y);
+                s1[v] = make_float2(f.z, f.w);
+                ns1[v] = make_float2(-f.z, -f.w);
+                c8[v] = make_float2(e.x, e.y);
+                z8[v] = make_float2(e.z, e.w);
             }
         }
-        auto rot_wait = [&](uint32_t bar, uint32_t parity) {   // one poller; the same answer for all 128 threads
+        auto rot_wait = [&](uint32_t bar, uint32_t parity) {   // one poller; the same answer for all 256 threads
             int go = 1;
             if (rt == 0) go = mbar_wait(bar, parity, abort_flag) ? 1 : 0;
             go = go && *abort_flag == 0;
             int all;
             asm volatile(
-                "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\t"
                 "selp.b32 %0, 1, 0, q;\n\t}"
                 : "=r"(all)
                 : "r"(go)
@@ -375,53 +415,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&bar_kready[st]));
                 break;
             }
-            const int np = info.n[p];
-            uint8_t* kb = sm + kOffK + st * 2 * kTile + (2 * p) * 1024 + (u & 1) * 8;
-            float C[4], S[4];
+            const int np = info.n[p] - 8 * s8;
+            uint8_t* kb = sm + kOffK + st * 2 * kTile + (2 * p + s8) * 1024 + (u & 1) * 8;
+            float2 C[2], S[2];
             if (ROT) {
                 const float4* b4 = reinterpret_cast<const float4*>(sm + kOffBase + st * kBaseBytes + p * 512) + 2 * u;
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     const float4 b = b4[v];
-                    C[2 * v] = b.x; C[2 * v + 1] = b.y;
-                    S[2 * v] = b.z; S[2 * v + 1] = b.w;
+                    C[v] = make_float2(b.x, b.y);
+                    S[v] = make_float2(b.z, b.w);
+                    if (!LOCAL) {
+                        const float2 cc = f2_sub(f2_mul(C[v], c8[v]), f2_mul(S[v], z8[v]));
+                        S[v] = f2_fma(S[v], c8[v], f2_mul(C[v], z8[v]));
+                        C[v] = cc;
+                    }
                 }
             }
-#pragma unroll 1
-            for (int s8 = 0; s8 < 2; ++s8) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint2* p1 = reinterpret_cast<uint2*>(kb + s8 * 1024 + j * 128 + (((u >> 1) ^ j) << 4));
-                    uint2* p2 = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p1) + kHalf);
-                    uint2 h1 = make_uint2(0, 0), h2 = h1, l1 = h1, l2 = h1;
-                    if (8 * s8 + j < np) {
-                        const uint2 a = *p1, z = *p2;
-                        float x[4] = {bf_lo(a.x), bf_hi(a.x), bf_lo(a.y), bf_hi(a.y)};
-                        float y[4] = {bf_lo(z.x), bf_hi(z.x), bf_lo(z.y), bf_hi(z.y)};
-                        if (ROT) {
+            for (int j = 0; j < 8; ++j) {
+                uint2* p1 = reinterpret_cast<uint2*>(kb + j * 128 + (((u >> 1) ^ j) << 4));
+                uint2* p2 = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p1) + kHalf);
+                uint2 h1 = make_uint2(0, 0), h2 = h1, l1 = h1, l2 = h1;
+                if (j < np) {   // no key in this slot: zeros, so that its scores stay finite
+                    const uint2 a = *p1, z = *p2;
+                    float2 x[2] = {make_float2(bf_lo(a.x), bf_hi(a.x)), make_float2(bf_lo(a.y), bf_hi(a.y))};
+                    float2 y[2] = {make_float2(bf_lo(z.x), bf_hi(z.x)), make_float2(bf_lo(z.y), bf_hi(z.y))};
+                    if (ROT) {
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                const float f = x[v] * C[v] - y[v] * S[v];
-                                y[v] = x[v] * S[v] + y[v] * C[v];
-                                x[v] = f;
-                            }
+                        for (int v = 0; v < 2; ++v) {
+                            const float2 f = f2_sub(f2_mul(x[v], C[v]), f2_mul(y[v], S[v]));
+                            y[v] = f2_fma(x[v], S[v], f2_mul(y[v], C[v]));
+                            x[v] = f;
                         }
-                        h1 = make_uint2(pack_h2(x[0], x[1]), pack_h2(x[2], x[3]));
-                        h2 = make_uint2(pack_h2(y[0], y[1]), pack_h2(y[2], y[3]));
-                        l1 = make_uint2(rest_h2(x[0], x[1], h1.x), rest_h2(x[2], x[3], h1.y));
-                        l2 = make_uint2(rest_h2(y[0], y[1], h2.x), rest_h2(y[2], y[3], h2.y));
                     }
-                    *p1 = h1;
-                    *p2 = h2;
-                    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p1) + kTile) = l1;
-                    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p2) + kTile) = l2;
-                    if (ROT && !LOCAL) {   // next slot: angle + theta
+                    h1 = make_uint2(pack_h2(x[0].x, x[0].y), pack_h2(x[1].x, x[1].y));
+                    h2 = make_uint2(pack_h2(y[0].x, y[0].y), pack_h2(y[1].x, y[1].y));
+                    l1 = make_uint2(rest_h2(x[0].x, x[0].y, h1.x), rest_h2(x[1].x, x[1].y, h1.y));
+                    l2 = make_uint2(rest_h2(y[0].x, y[0].y, h2.x), rest_h2(y[1].x, y[1].y, h2.y));
+                }
+                *p1 = h1;
+                *p2 = h2;
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p1) + kTile) = l1;
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p2) + kTile) = l2;
+                if (ROT && !LOCAL) {   // next slot: angle + theta
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const float cc = C[v] * c1[v] - S[v] * s1[v];
-                            S[v] = S[v] * c1[v] + C[v] * s1[v];
-                            C[v] = cc;
-                        }
+                    for (int v = 0; v < 2; ++v) {
+                        const float2 cc = f2_fma(C[v], c1[v], f2_mul(S[v], ns1[v]));
+                        S[v] = f2_fma(S[v], c1[v], f2_mul(C[v], s1[v]));
+                        C[v] = cc;
                     }
                 }
             }
@@ -495,7 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 x = P.stats[stats_at(P, Hkv, r, h, block, i >> 1, i & 1) + trow];
                     if (x.y > 0.f) Lsum += x.y * fast_exp2(x.x - M);
                 }
-                s_row[trow] = Lsum > 0.f ? make_float2(M, 1.f / Lsum) : make_float2(0.f, 0.f);
+                float* at = s_row + 4 * (trow >> 1) + (trow & 1);
+                at[0] = Lsum > 0.f ? -M : 0.f;
+                at[2] = Lsum > 0.f ? 1.f / Lsum : 0.f;
             }
             asm volatile("bar.sync 2, 256;" ::: "memory");
         }
@@ -531,23 +575,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t v[64];
-                    tmem_ld64(tl + 64 * hh, v);
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                for (int w = 0; w < 4; ++w) {   // pages 2w and 2w + 1
+                    uint32_t v[32];
+                    tmem_ld32(tl + 32 * w, v);
                     if (ALIBI) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
+                        for (int i = 0; i < 32; ++i)
                             v[i] = __float_as_uint(__uint_as_float(v[i]) +
-                                                   slope * (float)(dist[4 * hh + (i >> 4)] + (i & 15)));
+                                                   slope * (float)(dist[2 * w + (i >> 4)] + (i & 15)));
                     }
                     if (!wfull) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            v[i] = (vis[2 * hh + (i >> 5)] >> (i & 31)) & 1u ? v[i] : 0xff800000u;
+                        for (int i = 0; i < 32; ++i) v[i] = (vis[w] >> i) & 1u ? v[i] : 0xff800000u;
                     }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
+                    for (int i = 0; i < 16; ++i)
                         mx[i & 3] = fmax3(mx[i & 3], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if (top > m_run + kRescaleThreshold) {
@@ -555,10 +598,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m_run = top;
                     }
                     const float ref = m_run == -INFINITY ? 0.f : m_run;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) sum[i & 3] += fast_exp2(__uint_as_float(v[i]) - ref);
-                    l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 d = f2_sub(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                                make_float2(ref, ref));
+                        sum[i & 1] = f2_add(sum[i & 1], make_float2(fast_exp2(d.x), fast_exp2(d.y)));
+                    }
+                    const float2 both = f2_add(sum[0], sum[1]);
+                    l_run += both.x + both.y;
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -573,29 +621,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const bool wfull = __all_sync(0xffffffffu, c0 == 0);
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t v[64];
-                    tmem_ld64(tl + 64 * hh, v);
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t v[32];
+                    tmem_ld32(tl + 32 * w, v);
                     if (ALIBI) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) {
-                            const int c = 64 * hh + i, t = c / g;
+                        for (int i = 0; i < 32; ++i) {
+                            const int c = 32 * w + i, t = c / g;
                             v[i] = __float_as_uint(__uint_as_float(v[i]) + alibi_slope(h * g + c - t * g, Hq) * kLog2e *
                                                                                 (float)(pos - (m_lo + t)));
                         }
                     }
                     if (!wfull) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) v[i] = 64 * hh + i >= c0 ? v[i] : 0xff800000u;
+                        for (int i = 0; i < 32; ++i) v[i] = 32 * w + i >= c0 ? v[i] : 0xff800000u;
                     }
-                    const float4* rows = reinterpret_cast<const float4*>(s_row) + 32 * hh;
+                    const float4* rows = reinterpret_cast<const float4*>(s_row) + 16 * w;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float4 st = rows[i];   // (M, 1 / L) of columns 2i, 2i + 1
-                        sum[2 * (i & 1)] += fast_exp2(__uint_as_float(v[2 * i]) - st.x) * st.y;
-                        sum[2 * (i & 1) + 1] += fast_exp2(__uint_as_float(v[2 * i + 1]) - st.z) * st.w;
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 st = rows[i];   // -M, then 1 / L, of columns 2i, 2i + 1
+                        const float2 d = f2_add(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                                make_float2(st.x, st.y));
+                        sum[i & 1] = f2_fma(make_float2(fast_exp2(d.x), fast_exp2(d.y)), make_float2(st.z, st.w), sum[i & 1]);
                     }
                 }
                 tc_fence_before();
@@ -604,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int idx = j * kPagesPerTile + p;
                 if (idx < e1 - e0)
                     P.sums[((((size_t)block * P.requests + r) * P.cap + idx) * Hkv + h) * kPage + slot] =
-                        (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
         }
         if (PASS == 1)
