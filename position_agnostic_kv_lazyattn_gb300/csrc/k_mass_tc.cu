@@ -4,10 +4,9 @@
 // scores are, and keeping the scores (4 bytes each, against 0.75 ns of tensor time for 256
 // of them) would take more memory time than forming them again, so there are two passes over the
 // keys and a reduction:
-//   pass 1  S = Q K^T, thread = row: running maximum and sum per row
-//   pass 2  S^T = K Q^T (the same operands in shared memory, changed over), thread =
-//           key: the weights of its column summed in registers; one float per key and
-//           block of 128 rows goes to the workspace
+//   pass 1  running maximum and sum of each row (thread = row)
+//   pass 2  the rows' weights, summed per key: one float per key and block of 128
+//           rows goes to the workspace
 //   reduce  the row blocks' floats in order, plus decay * mass_in
 // No atomics: equal calls give equal bits.
 //
@@ -16,15 +15,20 @@
 // the rest), and the accumulator takes K_lo Q_hi, K_hi Q_lo, then K_hi Q_hi, small
 // ones first. That is 24 MMAs of 128 x 128 x 16 per 128 x 128 scores, and what bounds both passes.
 //
-// CTA = (request, KV head, 128 rows = (token, head of the group) pairs, share of the
-// tiles of 128 keys). Roles (20 warps):
+// CTA = (request, KV head, two blocks of 128 rows = (token, head of the group) pairs, share
+// of the tiles of 128 keys). Q is the MMAs' A operand in tensor memory: an MMA then
+// reads 4 KB of shared memory in its 64 cycles, not 8 (which is all that
+// the shared memory gives, with the rotation's own traffic on top), and the space goes to a third K
+// stage. Roles (20 warps):
 //   warp 0        producer: block table, TMA of K pages and of their position-table rows
 //   warp 1        TMEM owner, MMA issuer
-//   warps 4-11    two warpgroups, taking the tiles in turn (two S buffers); each builds
-//                 half of the dims of Q first
+//   warps 4-11    two warpgroups. Two row blocks: each builds its own block's Q and takes its
+//                 scores of every tile. One: they take the tiles of the one block in turn
 //   warps 12-19   rotation: thread = (page, half of its slots, 4 frequencies), bf16 in
 //                 place to hi, lo beside it
-// Two K stages of 64 KB (hi, lo), Q 64 KB. Every wait is bounded, as in the prefill kernel.
+// Column sums of pass 2: TMEM is read in the fragment layout, where a thread holds 4 rows of
+// the same 8 columns; it adds those, 7 shuffles join the 8 threads of a column, and the
+// four warps meet in shared memory. Every wait is bounded, as in the prefill kernel.
 #include <limits.h>
 
 #include "internal.h"
@@ -37,20 +41,20 @@ namespace {
 using namespace tc;
 
 constexpr int kD = 128;
-constexpr int kTileM = 128;                        // rows per CTA
+constexpr int kTileM = 128;                        // rows per block; two blocks per CTA
 constexpr int kN = 128;                            // keys per tile
 constexpr int kPagesPerTile = kN / kPage;          // 8
-constexpr int kStages = 2;
-constexpr int kInfoSlots = 4;
+constexpr int kStages = 3;
+constexpr int kInfoSlots = 8;                      // the scores of tile k - 8 were read before tile k's copies start
 constexpr int kThreads = 640;
 constexpr int kHalf = kTileM * 128;                // 16 KB: 64 dims of 128 rows or keys
 constexpr int kTile = 2 * kHalf;                   // 32 KB: one fp16 operand tile
 constexpr int kBaseBytes = kPagesPerTile * 512;    // 8 position-table rows
-constexpr int kOffQ = 0;                           // Q hi, Q lo
-constexpr int kOffK = kOffQ + 2 * kTile;           // stages of (K hi, K lo)
+constexpr int kOffK = 0;                           // stages of (K hi, K lo)
 constexpr int kOffBase = kOffK + kStages * 2 * kTile;
-constexpr int kSmemBytes = kOffBase + kStages * kBaseBytes + 1024;
-constexpr uint32_t kTmemCols = 256;                // two S buffers
+constexpr int kOffSum = kOffBase + kStages * kBaseBytes;   // pass 2: [warpgroup][tile parity][warp][key] column sums
+constexpr int kSmemBytes = kOffSum + 2 * 2 * 4 * kN * 4 + 1024;
+constexpr uint32_t kTmemCols = 512;                // S buffers of 128 columns; from 256 on Q hi, Q lo (64 each) of both blocks
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;          // log2 units
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -73,11 +77,11 @@ struct MassParams {
     int32_t g;
     int32_t oob_row;
     int32_t row_blocks;           // rows of the position table's 16-row view
-    int32_t blocks;               // row blocks per request (host bound)
+    int32_t blocks;               // row blocks per request (host bound), an even number
     int32_t splits;
     int32_t cap;                  // entries per request (host bound)
     int32_t requests;
-    float2* stats;                // [r][h][block][split][warpgroup][128] (reference maximum, sum)
+    float2* stats;                // [r][h][block][split][2][128] (reference maximum, sum)
     float* sums;                  // [block][r][cap][Hkv][16]
 };
 
@@ -155,8 +159,8 @@ __device__ __forceinline__ int usable_local(const PoolView& pv, uint64_t e, int 
     return n > 0 && (delta < 0 || delta > entry_start(e) || delta >= pv.max_position) ? -1 : n;
 }
 
-__device__ __forceinline__ size_t stats_at(const MassParams& P, int hkv, int r, int h, int block, int split, int wg) {
-    return ((((size_t)r * hkv + h) * P.blocks + block) * P.splits + split) * (2 * kTileM) + (size_t)wg * kTileM;
+__device__ __forceinline__ size_t stats_at(const MassParams& P, int hkv, int r, int h, int block, int split, int part) {
+    return ((((size_t)r * hkv + h) * P.blocks + block) * P.splits + split) * (2 * kTileM) + (size_t)part * kTileM;
 }
 
 template <bool PREROT, bool LOCAL, bool INTER, bool ALIBI, int PASS>
@@ -172,23 +176,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ TileInfo s_info[kInfoSlots];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ __align__(16) float s_row[PASS == 2 ? 2 * kTileM : 4];   // pass 2: (-M, -M, 1 / L, 1 / L) of rows 2i, 2i + 1
+    __shared__ float2 s_row[PASS == 2 ? 2 * kTileM : 1];   // pass 2: (M, 1 / L) of each row
 
-    const int block = blockIdx.x / P.splits, split = blockIdx.x - block * P.splits;
+    const int pair = blockIdx.x / P.splits, split = blockIdx.x - pair * P.splits;
     const int h = blockIdx.y, r = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = P.g, Hq = pv.hq, Hkv = pv.hkv;
     const int TQ = kTileM / g;
     const int q0 = P.q_offsets[r], q1 = P.q_offsets[r + 1];
-    const int i0 = block * TQ;
+    const int i0 = 2 * pair * TQ;
     const int tokens = min(q1 - q0, P.max_rows);
     if (i0 >= tokens) return;
     if (q1 > P.total_q) {
         if (threadIdx.x == 0) record_error(pv.status, LAZYATTN_ERANGE);
         return;
     }
-    const int ntok = min(TQ, tokens - i0);
-    const int m_lo = P.q_start[r] + i0, m_hi = m_lo + ntok - 1;
+    const int ntok = min(2 * TQ, tokens - i0);
+    const bool two = ntok > TQ;                // the second block has rows
+    const int m_hi = P.q_start[r] + i0 + ntok - 1;
     const int e0 = P.entry_offsets[r], e1 = min(P.entry_offsets[r + 1], e0 + P.cap);
     const int t_all = e1 > e0 ? (e1 - e0 + kPagesPerTile - 1) / kPagesPerTile : 0;
     const int chunk = (t_all + P.splits - 1) / P.splits;
@@ -341,29 +346,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
             const uint32_t id = idesc_f16(kTileM, kN, 0, 0, 0);
-            const uint64_t dq = sdesc_sw128(smem_u32(sm + kOffQ), 16, 1024);
             const uint64_t dk = sdesc_sw128(smem_u32(sm + kOffK), 16, 1024);
-            bool ok = mbar_wait(smem_u32(&bar_qready), 0, abort_flag);
-            for (int k = 0; ok; ++k) {
-                const int st = k % kStages, ph = (k / kStages) & 1, b = k & 1;
-                ok = mbar_wait(smem_u32(&bar_kready[st]), ph, abort_flag);
-                if (!ok || s_info[k & (kInfoSlots - 1)].j < 0) break;
-                ok = k < 2 || mbar_wait(smem_u32(&bar_sempty[b]), ((k >> 1) - 1) & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t ks = dk + (uint64_t)(st * (2 * kTile >> 4));
+            // S buffer b gets the scores of row block i
+            auto issue = [&](int b, int i, uint64_t ks) {
 #pragma unroll
                 for (int part = 0; part < 3; ++part) {   // K_lo Q_hi, K_hi Q_lo, K_hi Q_hi
                     const uint64_t ka = ks + (part == 0 ? (uint64_t)(kTile >> 4) : 0);
-                    const uint64_t qa = dq + (part == 1 ? (uint64_t)(kTile >> 4) : 0);
+                    const uint32_t qa = tmem + 256 + i * 128 + (part == 1 ? 64 : 0);
 #pragma unroll
-                    for (int t = 0; t < kD / 16; ++t) {
-                        const uint64_t o = (uint64_t)(((t >> 2) * kHalf + (t & 3) * 32) >> 4);
-                        umma_f16(tmem + b * 128, (PASS == 1 ? qa : ka) + o, (PASS == 1 ? ka : qa) + o, id,
-                                 part > 0 || t > 0 ? 1u : 0u);
-                    }
+                    for (int t = 0; t < kD / 16; ++t)
+                        umma_f16_ts(tmem + b * 128, qa + 8 * t, ka + (uint64_t)(((t >> 2) * kHalf + (t & 3) * 32) >> 4), id,
+                                    part > 0 || t > 0 ? 1u : 0u);
                 }
                 umma_commit(smem_u32(&bar_sfull[b]));
+            };
+            bool ok = mbar_wait(smem_u32(&bar_qready), 0, abort_flag);
+            tc_fence_after();
+            for (int k = 0; ok; ++k) {
+                const int st = k % kStages;
+                ok = mbar_wait(smem_u32(&bar_kready[st]), (k / kStages) & 1, abort_flag);
+                if (!ok || s_info[k & (kInfoSlots - 1)].j < 0) break;
+                const uint64_t ks = dk + (uint64_t)(st * (2 * kTile >> 4));
+                if (two) {
+                    for (int i = 0; i < 2 && ok; ++i) {
+                        ok = k < 1 || mbar_wait(smem_u32(&bar_sempty[i]), (k - 1) & 1, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue(i, i, ks);
+                    }
+                    if (!ok) break;
+                } else {
+                    ok = k < 2 || mbar_wait(smem_u32(&bar_sempty[k & 1]), ((k >> 1) - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue(k & 1, 0, ks);
+                }
                 umma_commit(smem_u32(&bar_kempty[st]));
             }
             umma_commit(smem_u32(&bar_drain));
@@ -472,62 +489,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&bar_kready[st]));
         }
     } else if (warp >= 4) {
-        // ------------------------------------------------------------ rows / keys
+        // ------------------------------------------------------------ rows
         const int wg = (warp - 4) >> 2, quarter = warp & 3;
-        const int trow = 32 * quarter + lane;      // row of Q (pass 1), key of the tile (pass 2): TMEM lane
-        const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16) + wg * 128;
+        const int qi = two ? wg : 0;               // the row block this warpgroup works on
+        const int block = 2 * pair + qi;
+        const int trow = 32 * quarter + lane;      // row of the block = TMEM lane
+        const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t ts = tl + wg * 128;         // its S buffer
+        const int m0 = P.q_start[r] + block * TQ;  // position of the block's first token
+        const int btok = min(TQ, tokens - block * TQ);
         const int t_local = trow / g, jh = trow - t_local * g;
-        const int m_row = m_lo + t_local;
-        bool row_valid = t_local < ntok;
+        const int m_row = m0 + t_local;
+        bool row_valid = t_local < btok;
         if (row_valid && (m_row < 0 || m_row >= pv.max_position)) {
             record_error(pv.status, LAZYATTN_ERANGE);
             row_valid = false;
         }
-        {   // Q: this warpgroup's 32 dims of each half of its row, rotated at m_row and scaled, hi and lo
-            uint8_t* qsm = sm + kOffQ;
+        if (two || wg == 0) {   // the row of Q, rotated at m_row and scaled, as hi and lo: dims 2c, 2c + 1 in column c
             const float sc = kLog2e * pv.qk_scale;
-            const __nv_bfloat16* qp = P.q + ((size_t)(q0 + i0 + t_local) * Hq + (size_t)h * g + jh) * kD;
+            const __nv_bfloat16* qp = P.q + ((size_t)(q0 + block * TQ + t_local) * Hq + (size_t)h * g + jh) * kD;
             const float* cs = reinterpret_cast<const float*>(pv.rope + (size_t)(row_valid ? m_row : 0) * (kD / 2));
+            const uint32_t tq = tl + 256 + qi * 128;
+#pragma unroll 1
+            for (int h4 = 0; h4 < 2; ++h4) {       // 32 dims of each half
+                uint32_t hi1[16], hi2[16], lo1[16], lo2[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int u = 4 * wg + i;
-                uint4 h1 = make_uint4(0, 0, 0, 0), h2 = h1, l1 = h1, l2 = h1;
-                if (row_valid) {
-                    uint4 a = __ldg(reinterpret_cast<const uint4*>(qp + (INTER ? 16 * u : 8 * u)));
-                    uint4 b = __ldg(reinterpret_cast<const uint4*>(qp + (INTER ? 16 * u + 8 : 64 + 8 * u)));
-                    if (INTER) deinterleave16(a, b, a, b);
-                    float x1[8], x2[8], n2 = 0.f;
-                    unpack8(a, x1);
-                    unpack8(b, x2);
+                for (int i = 0; i < 4; ++i) {
+                    const int u = 4 * h4 + i;
+                    uint4 a1 = make_uint4(0, 0, 0, 0), a2 = a1, b1 = a1, b2 = a1;
+                    if (row_valid) {
+                        uint4 a = __ldg(reinterpret_cast<const uint4*>(qp + (INTER ? 16 * u : 8 * u)));
+                        uint4 b = __ldg(reinterpret_cast<const uint4*>(qp + (INTER ? 16 * u + 8 : 64 + 8 * u)));
+                        if (INTER) deinterleave16(a, b, a, b);
+                        float x1[8], x2[8], n2 = 0.f;
+                        unpack8(a, x1);
+                        unpack8(b, x2);
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) n2 = fmaxf(n2, fmaf(x1[v], x1[v], x2[v] * x2[v]));
-                    if (!(n2 * sc * sc <= kMaxPairNorm2)) record_error(pv.status, LAZYATTN_ERANGE);
-                    const float4* c4 = reinterpret_cast<const float4*>(cs + 16 * u);
+                        for (int v = 0; v < 8; ++v) n2 = fmaxf(n2, fmaf(x1[v], x1[v], x2[v] * x2[v]));
+                        if (!(n2 * sc * sc <= kMaxPairNorm2)) record_error(pv.status, LAZYATTN_ERANGE);
+                        const float4* c4 = reinterpret_cast<const float4*>(cs + 16 * u);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const float4 f = ALIBI ? make_float4(1.f, 0.f, 1.f, 0.f) : __ldg(c4 + v);
-                        const float a0 = x1[2 * v], z0 = x2[2 * v], a1 = x1[2 * v + 1], z1 = x2[2 * v + 1];
-                        x1[2 * v] = (a0 * f.x - z0 * f.y) * sc;
-                        x2[2 * v] = (a0 * f.y + z0 * f.x) * sc;
-                        x1[2 * v + 1] = (a1 * f.z - z1 * f.w) * sc;
-                        x2[2 * v + 1] = (a1 * f.w + z1 * f.z) * sc;
+                        for (int v = 0; v < 4; ++v) {
+                            const float4 f = ALIBI ? make_float4(1.f, 0.f, 1.f, 0.f) : __ldg(c4 + v);
+                            const float a0 = x1[2 * v], z0 = x2[2 * v], a1_ = x1[2 * v + 1], z1 = x2[2 * v + 1];
+                            x1[2 * v] = (a0 * f.x - z0 * f.y) * sc;
+                            x2[2 * v] = (a0 * f.y + z0 * f.x) * sc;
+                            x1[2 * v + 1] = (a1_ * f.z - z1 * f.w) * sc;
+                            x2[2 * v + 1] = (a1_ * f.w + z1 * f.z) * sc;
+                        }
+                        split8(x1, a1, b1);
+                        split8(x2, a2, b2);
                     }
-                    split8(x1, h1, l1);
-                    split8(x2, h2, l2);
+                    hi1[4 * i] = a1.x; hi1[4 * i + 1] = a1.y; hi1[4 * i + 2] = a1.z; hi1[4 * i + 3] = a1.w;
+                    hi2[4 * i] = a2.x; hi2[4 * i + 1] = a2.y; hi2[4 * i + 2] = a2.z; hi2[4 * i + 3] = a2.w;
+                    lo1[4 * i] = b1.x; lo1[4 * i + 1] = b1.y; lo1[4 * i + 2] = b1.z; lo1[4 * i + 3] = b1.w;
+                    lo2[4 * i] = b2.x; lo2[4 * i + 1] = b2.y; lo2[4 * i + 2] = b2.z; lo2[4 * i + 3] = b2.w;
                 }
-                const uint32_t o = sw128_offset(trow, u);
-                *reinterpret_cast<uint4*>(qsm + o) = h1;
-                *reinterpret_cast<uint4*>(qsm + kHalf + o) = h2;
-                *reinterpret_cast<uint4*>(qsm + kTile + o) = l1;
-                *reinterpret_cast<uint4*>(qsm + kTile + kHalf + o) = l2;
+                __syncwarp();
+                tmem_st16(tq + 16 * h4, hi1);
+                tmem_st16(tq + 32 + 16 * h4, hi2);
+                tmem_st16(tq + 64 + 16 * h4, lo1);
+                tmem_st16(tq + 96 + 16 * h4, lo2);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar_qready));
+            tmem_wait_st();
         }
-        if (PASS == 2) {   // merge the rows' statistics: warpgroup 0, one row a thread
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_qready));
+
+        // pass 2: this thread's four rows in the fragment layout: 32 quarter + lane / 4 + 8 f
+        float nM[4], inv[4], slope4[4];
+        int m4[4];
+        int m_see = INT_MAX;   // smallest position of the warp's rows with weights
+        if (PASS == 2) {
             grid_dep_wait();
-            if (wg == 0) {
+            {   // merge the row's statistics
                 float M = -INFINITY, Lsum = 0.f;
                 for (int i = 0; i < 2 * P.splits; ++i) {
                     const float2 x = P.stats[stats_at(P, Hkv, r, h, block, i >> 1, i & 1) + trow];
@@ -537,24 +573,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 x = P.stats[stats_at(P, Hkv, r, h, block, i >> 1, i & 1) + trow];
                     if (x.y > 0.f) Lsum += x.y * fast_exp2(x.x - M);
                 }
-                float* at = s_row + 4 * (trow >> 1) + (trow & 1);
-                at[0] = Lsum > 0.f ? -M : 0.f;
-                at[2] = Lsum > 0.f ? 1.f / Lsum : 0.f;
+                s_row[wg * kTileM + trow] = Lsum > 0.f ? make_float2(M, 1.f / Lsum) : make_float2(0.f, 0.f);
             }
-            asm volatile("bar.sync 2, 256;" ::: "memory");
+            __syncwarp();      // a warp reads the rows of its own lanes only
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const int row = 32 * quarter + (lane >> 2) + 8 * f;
+                const float2 x = s_row[wg * kTileM + row];
+                nM[f] = x.y > 0.f ? -x.x : -INFINITY;   // a row that sees no key: weights 0 whatever its scores
+                inv[f] = x.y;
+                m4[f] = m0 + row / g;
+                slope4[f] = ALIBI ? alibi_slope(h * g + row % g, Hq) * kLog2e : 0.f;
+                if (x.y > 0.f) m_see = min(m_see, m4[f]);
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) m_see = min(m_see, __shfl_xor_sync(0xffffffffu, m_see, o));
         }
 
         float m_run = -INFINITY, l_run = 0.f;
         bool ok = true;
-        for (int k = wg;; k += 2) {
+        const float slope = ALIBI ? alibi_slope(h * g + jh, Hq) * kLog2e : 0.f;
+        for (int k = two ? 0 : wg, use = 0;; k += two ? 1 : 2, ++use) {
             const int is = k & (kInfoSlots - 1);
             ok = mbar_wait(smem_u32(&bar_info[is]), (k / kInfoSlots) & 1, abort_flag);
-            if (!ok) break;
             const TileInfo& info = s_info[is];
-            const int j = info.j;
-            if (j < 0) break;
+            const int j = ok ? info.j : -1;
             if (PASS == 1) {
-                const float slope = ALIBI ? alibi_slope(h * g + jh, Hq) * kLog2e : 0.f;
+                if (j < 0) break;
                 const bool wfull = __all_sync(0xffffffffu, row_valid && m_row >= info.full_from);
                 uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
 #pragma unroll
@@ -568,21 +613,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     vis[w] = bits;
                 }
-                int dist[kPagesPerTile];   // ALiBi: position of each page's slot 0 relative to the row
-#pragma unroll
-                for (int p = 0; p < kPagesPerTile; ++p) dist[p] = ALIBI ? info.start[p] - m_row : 0;
-                ok = mbar_wait(smem_u32(&bar_sfull[wg]), (k >> 1) & 1, abort_flag);
+                ok = mbar_wait(smem_u32(&bar_sfull[wg]), use & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {   // pages 2w and 2w + 1
                     uint32_t v[32];
-                    tmem_ld32(tl + 32 * w, v);
+                    tmem_ld32(ts + 32 * w, v);
                     if (ALIBI) {
+                        const int d0 = info.start[2 * w] - m_row, d1 = info.start[2 * w + 1] - m_row;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            v[i] = __float_as_uint(__uint_as_float(v[i]) +
-                                                   slope * (float)(dist[2 * w + (i >> 4)] + (i & 15)));
+                            v[i] = __float_as_uint(__uint_as_float(v[i]) + slope * (float)((i < 16 ? d0 : d1) + (i & 15)));
                     }
                     if (!wfull) {
 #pragma unroll
@@ -612,53 +654,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar_sempty[wg]));
             } else {
-                // key trow: columns c >= c0 hold the rows that see it (positions go up with the row)
-                const int p = trow >> 4, slot = trow & 15;
-                const int pos = info.start[p] + slot;
-                const int64_t before = (int64_t)pos - m_lo;
-                const int c0 = slot < info.n[p] ? (int)min((int64_t)kTileM, max((int64_t)0, before * g)) : kTileM;
-                ok = mbar_wait(smem_u32(&bar_sfull[wg]), (k >> 1) & 1, abort_flag);
-                if (!ok) break;
+                const bool full = j >= 0 && info.full_from <= m_see;   // every key is seen by every row with weights
+                float* cols = reinterpret_cast<float*>(sm + kOffSum) + ((wg * 2 + (use & 1)) * 4 + quarter) * kN;
+                ok = j >= 0 && mbar_wait(smem_u32(&bar_sfull[wg]), use & 1, abort_flag);
                 tc_fence_after();
-                const bool wfull = __all_sync(0xffffffffu, c0 == 0);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t v[32];
-                    tmem_ld32(tl + 32 * w, v);
-                    if (ALIBI) {
+                for (int w = 0; w < 4 && ok; ++w) {
+                    uint32_t v[2][16];
+                    tmem_ld_frag32(ts + 32 * w, v[0]);
+                    tmem_ld_frag32(ts + 32 * w + (16u << 16), v[1]);
+                    float2 acc[4];   // columns 32 w + 8 i + 2 (lane % 4), + 1
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int c = 32 * w + i, t = c / g;
-                            v[i] = __float_as_uint(__uint_as_float(v[i]) + alibi_slope(h * g + c - t * g, Hq) * kLog2e *
-                                                                                (float)(pos - (m_lo + t)));
+                    for (int i = 0; i < 4; ++i) {
+                        acc[i] = make_float2(0.f, 0.f);
+                        const int p = 2 * w + (i >> 1), s0 = 8 * (i & 1) + 2 * (lane & 3);
+                        const int pos = (ALIBI || !full) ? info.start[p] + s0 : 0;
+                        const int n = full ? kPage : info.n[p];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            float2 d = make_float2(__uint_as_float(v[f >> 1][4 * i + 2 * (f & 1)]),
+                                                   __uint_as_float(v[f >> 1][4 * i + 2 * (f & 1) + 1]));
+                            if (ALIBI) {
+                                d.x += slope4[f] * (float)(pos - m4[f]);
+                                d.y += slope4[f] * (float)(pos + 1 - m4[f]);
+                            }
+                            d = f2_add(d, make_float2(nM[f], nM[f]));
+                            if (!full) {
+                                d.x = s0 < n && pos <= m4[f] ? d.x : -INFINITY;
+                                d.y = s0 + 1 < n && pos + 1 <= m4[f] ? d.y : -INFINITY;
+                            }
+                            acc[i] = f2_fma(make_float2(fast_exp2(d.x), fast_exp2(d.y)), make_float2(inv[f], inv[f]), acc[i]);
                         }
                     }
-                    if (!wfull) {
+                    // join the 8 threads of a column (lane / 4), halving the columns each time
+                    float a4[4], a2[2];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 32 * w + i >= c0 ? v[i] : 0xff800000u;
+                    for (int i = 0; i < 2; ++i) {   // lane bit 4 picks column groups 2, 3
+                        const bool up = lane & 16;
+                        const float2 give = up ? acc[i] : acc[i + 2], keep = up ? acc[i + 2] : acc[i];
+                        a4[2 * i] = keep.x + __shfl_xor_sync(0xffffffffu, give.x, 16);
+                        a4[2 * i + 1] = keep.y + __shfl_xor_sync(0xffffffffu, give.y, 16);
                     }
-                    const float4* rows = reinterpret_cast<const float4*>(s_row) + 16 * w;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float4 st = rows[i];   // -M, then 1 / L, of columns 2i, 2i + 1
-                        const float2 d = f2_add(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                                                make_float2(st.x, st.y));
-                        sum[i & 1] = f2_fma(make_float2(fast_exp2(d.x), fast_exp2(d.y)), make_float2(st.z, st.w), sum[i & 1]);
+                    for (int i = 0; i < 2; ++i) {   // lane bit 3: the second group of the two
+                        const bool up = lane & 8;
+                        a2[i] = (up ? a4[2 + i] : a4[i]) + __shfl_xor_sync(0xffffffffu, up ? a4[i] : a4[2 + i], 8);
                     }
+                    const bool up = lane & 4;       // lane bit 2: the second column of the pair
+                    const float a1 = (up ? a2[1] : a2[0]) + __shfl_xor_sync(0xffffffffu, up ? a2[0] : a2[1], 4);
+                    cols[32 * w + ((lane >> 4) & 1) * 16 + ((lane >> 3) & 1) * 8 + 2 * (lane & 3) + ((lane >> 2) & 1)] = a1;
                 }
+                const int idx = j * kPagesPerTile + (trow >> 4);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_sempty[wg]));
-                const int idx = j * kPagesPerTile + p;
+                if (ok && lane == 0) mbar_arrive(smem_u32(&bar_sempty[wg]));
+                // The four warps meet (the other parity's buffer is free: all have passed the last
+                // meeting). A warp that gave up or saw the last tile says so here and all leave
+                // together: none is left waiting.
+                int all_ok;
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+                    "selp.b32 %0, 1, 0, q;\n\t}"
+                    : "=r"(all_ok)
+                    : "r"(ok ? 1 : 0), "r"(2 + wg)
+                    : "memory");
+                if (!all_ok) break;
+                const float* all = reinterpret_cast<const float*>(sm + kOffSum) + (wg * 2 + (use & 1)) * 4 * kN + trow;
                 if (idx < e1 - e0)
-                    P.sums[((((size_t)block * P.requests + r) * P.cap + idx) * Hkv + h) * kPage + slot] =
-                        (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    P.sums[((((size_t)block * P.requests + r) * P.cap + idx) * Hkv + h) * kPage + (trow & 15)] =
+                        (all[0] + all[kN]) + (all[2 * kN] + all[3 * kN]);
             }
         }
-        if (PASS == 1)
-            P.stats[stats_at(P, Hkv, r, h, block, split, wg) + trow] =
-                make_float2(m_run == -INFINITY ? 0.f : m_run, ok && row_valid ? l_run : 0.f);
+        if (PASS == 1) {
+            // two blocks: each has one part, the other stays empty; one block: a part from each warpgroup
+            const float2 x = make_float2(m_run == -INFINITY ? 0.f : m_run, ok && row_valid ? l_run : 0.f);
+            P.stats[stats_at(P, Hkv, r, h, block, split, two ? 0 : wg) + trow] = x;
+            if (two) P.stats[stats_at(P, Hkv, r, h, block, split, 1) + trow] = make_float2(0.f, 0.f);
+        }
     }
 
     tc_fence_before();
@@ -716,13 +788,13 @@ struct MassWs {
     size_t sums_off, total;
 };
 
-// CTAs per (request, KV head, row block): the split with the least time by waves of
+// CTAs per (request, KV head, two row blocks): the split with the least time by waves of
 // CTAs, each its tiles plus a start and an end of about four tiles' time; shares of 4 tiles or more.
 MassWs mass_ws(const lazyattn_pool& p, const lazyattn_batch& b) {
     MassWs w;
     const int g = p.d.n_q_heads / p.d.n_kv_heads, TQ = kTileM / g;
-    w.blocks = std::max(1, (b.max_q_len + TQ - 1) / TQ);
-    const int64_t items = (int64_t)b.num_requests * p.d.n_kv_heads * w.blocks;
+    w.blocks = 2 * std::max(1, (b.max_q_len + 2 * TQ - 1) / (2 * TQ));
+    const int64_t items = (int64_t)b.num_requests * p.d.n_kv_heads * (w.blocks / 2);
     const int64_t T = ((int64_t)b.max_entries + kPagesPerTile - 1) / kPagesPerTile;
     const int64_t sms = p.sm_count > 0 ? p.sm_count : 1;
     w.splits = 1;
@@ -735,7 +807,7 @@ MassWs mass_ws(const lazyattn_pool& p, const lazyattn_batch& b) {
             w.splits = s;
         }
     }
-    w.sums_off = up256((size_t)items * w.splits * 2 * kTileM * sizeof(float2));
+    w.sums_off = up256((size_t)items * 2 * w.splits * 2 * kTileM * sizeof(float2));
     w.total = w.sums_off + up256((size_t)w.blocks * b.num_requests * (size_t)std::max(b.max_entries, 1) *
                                  p.d.n_kv_heads * kPage * sizeof(float));
     return w;
@@ -784,7 +856,7 @@ int launch_prefill_mass_bf16(const lazyattn_pool& p, const lazyattn_batch& b, co
     const bool prerot = (b.flags & LAZYATTN_KEYS_PREROTATED) != 0, inter = p.d.rope_interleaved != 0;
     const bool local = p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL, alibi = p.d.position_encoding == LAZYATTN_POS_ALIBI;
     if (b.total_q > 0 && b.max_q_len > 0) {
-        const dim3 grid(w.blocks * w.splits, p.d.n_kv_heads, b.num_requests);
+        const dim3 grid(w.blocks / 2 * w.splits, p.d.n_kv_heads, b.num_requests);
         mass_kernel_for<1>(prerot, local, inter, alibi)<<<grid, kThreads, kSmemBytes, stream>>>(p.kmap, p.kmap4, p.kmap8,
                                                                                                 p.rmap, p.view(), P);
         if (cudaGetLastError() != cudaSuccess ||
