@@ -31,6 +31,8 @@
 // four warps meet in shared memory. Every wait is bounded, as in the prefill kernel.
 #include <limits.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "tc_ptx.cuh"
 
@@ -598,28 +600,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait(smem_u32(&bar_info[is]), (k / kInfoSlots) & 1, abort_flag);
             const TileInfo& info = s_info[is];
             const int j = ok ? info.j : -1;
+            // The S buffer is free once its last columns are in registers: the next MMAs overlap
+            // the arithmetic on those. (The tile info stays: its slot is reused 8 tiles on.)
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_sempty[wg]));
+            };
             if (PASS == 1) {
                 if (j < 0) break;
                 const bool wfull = __all_sync(0xffffffffu, row_valid && m_row >= info.full_from);
-                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-#pragma unroll
-                for (int w = 0; w < 4 && !wfull; ++w) {
-                    uint32_t bits = 0;
-#pragma unroll
-                    for (int hp = 0; hp < 2; ++hp) {
-                        const int p = 2 * w + hp;
-                        const int l = row_valid ? max(min(info.n[p], m_row - info.start[p] + 1), 0) : 0;
-                        bits |= ((1u << l) - 1u) << (16 * hp);
-                    }
-                    vis[w] = bits;
-                }
                 ok = mbar_wait(smem_u32(&bar_sfull[wg]), use & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1   // (unrolled, a pass of few tiles spends its time fetching instructions)
                 for (int w = 0; w < 4; ++w) {   // pages 2w and 2w + 1
                     uint32_t v[32];
                     tmem_ld32(ts + 32 * w, v);
+                    if (w == 3) release();
                     if (ALIBI) {
                         const int d0 = info.start[2 * w] - m_row, d1 = info.start[2 * w + 1] - m_row;
 #pragma unroll
@@ -627,8 +625,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             v[i] = __float_as_uint(__uint_as_float(v[i]) + slope * (float)((i < 16 ? d0 : d1) + (i & 15)));
                     }
                     if (!wfull) {
+                        uint32_t vis = 0;   // bit i: the row sees the key of column i
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = (vis[w] >> i) & 1u ? v[i] : 0xff800000u;
+                        for (int hp = 0; hp < 2; ++hp) {
+                            const int p = 2 * w + hp;
+                            const int l = row_valid ? max(min(info.n[p], m_row - info.start[p] + 1), 0) : 0;
+                            vis |= ((1u << l) - 1u) << (16 * hp);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = (vis >> i) & 1u ? v[i] : 0xff800000u;
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -650,26 +655,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 both = f2_add(sum[0], sum[1]);
                     l_run += both.x + both.y;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_sempty[wg]));
             } else {
                 const bool full = j >= 0 && info.full_from <= m_see;   // every key is seen by every row with weights
                 float* cols = reinterpret_cast<float*>(sm + kOffSum) + ((wg * 2 + (use & 1)) * 4 + quarter) * kN;
                 ok = j >= 0 && mbar_wait(smem_u32(&bar_sfull[wg]), use & 1, abort_flag);
                 tc_fence_after();
-#pragma unroll
-                for (int w = 0; w < 4 && ok; ++w) {
+                // two copies of the work, so that a tile without a hidden key tests nothing
+                auto weights = [&](auto FULL) {
+#pragma unroll 1
+                for (int w = 0; w < 4; ++w) {
                     uint32_t v[2][16];
                     tmem_ld_frag32(ts + 32 * w, v[0]);
                     tmem_ld_frag32(ts + 32 * w + (16u << 16), v[1]);
+                    if (w == 3) release();
                     float2 acc[4];   // columns 32 w + 8 i + 2 (lane % 4), + 1
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         acc[i] = make_float2(0.f, 0.f);
                         const int p = 2 * w + (i >> 1), s0 = 8 * (i & 1) + 2 * (lane & 3);
-                        const int pos = (ALIBI || !full) ? info.start[p] + s0 : 0;
-                        const int n = full ? kPage : info.n[p];
+                        const int pos = (ALIBI || !FULL) ? info.start[p] + s0 : 0;
+                        const int n = FULL ? kPage : info.n[p];
 #pragma unroll
                         for (int f = 0; f < 4; ++f) {
                             float2 d = make_float2(__uint_as_float(v[f >> 1][4 * i + 2 * (f & 1)]),
@@ -679,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 d.y += slope4[f] * (float)(pos + 1 - m4[f]);
                             }
                             d = f2_add(d, make_float2(nM[f], nM[f]));
-                            if (!full) {
+                            if (!FULL) {
                                 d.x = s0 < n && pos <= m4[f] ? d.x : -INFINITY;
                                 d.y = s0 + 1 < n && pos + 1 <= m4[f] ? d.y : -INFINITY;
                             }
@@ -704,10 +709,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float a1 = (up ? a2[1] : a2[0]) + __shfl_xor_sync(0xffffffffu, up ? a2[0] : a2[1], 4);
                     cols[32 * w + ((lane >> 4) & 1) * 16 + ((lane >> 3) & 1) * 8 + 2 * (lane & 3) + ((lane >> 2) & 1)] = a1;
                 }
+                };
+                if (ok) {
+                    if (full) weights(std::true_type{});
+                    else weights(std::false_type{});
+                }
                 const int idx = j * kPagesPerTile + (trow >> 4);
-                tc_fence_before();
-                __syncwarp();
-                if (ok && lane == 0) mbar_arrive(smem_u32(&bar_sempty[wg]));
                 // The four warps meet (the other parity's buffer is free: all have passed the last
                 // meeting). A warp that gave up or saw the last tile says so here and all leave
                 // together: none is left waiting.
