@@ -292,6 +292,7 @@ int launch_mass_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void
                      cudaStream_t stream);
 
 // Eviction: selection and copy.
+int evict_init();
 int launch_evict(const lazyattn_pool& p, const lazyattn_batch& b, const float* mass, int32_t budget, int32_t sinks,
                  int32_t recent, uint64_t* dst_entries, const int32_t* dst_offsets, int32_t* kept, float* dst_mass,
                  cudaStream_t stream);

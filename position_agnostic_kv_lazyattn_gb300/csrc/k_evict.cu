@@ -1,13 +1,25 @@
 // Eviction by accumulated attention weight: per (request, KV head), choose the
 // tokens to keep and copy their K and V into the request's new pages.
 //
-// One block per (KV head, request). Tokens are numbered in table order. The
-// k-th largest mass among the tokens that are neither sinks nor recent is found by
-// a radix select, most significant byte first, over the masses as ordered
-// integers; of the tokens equal to it the earliest are taken. The kept tokens'
-// places go to `kept` in order, then each is replaced by the token's position as
-// its rows are copied.
+// One cluster of 1..8 blocks per (KV head, request); each block has a contiguous
+// share of the table's entries. Tokens are numbered in table order. The k-th
+// largest mass among the tokens that are neither sinks nor recent is found by a radix
+// select over the masses as ordered integers, 11 bits at a time: every block counts its share
+// into a histogram in shared memory, and every block reads all the cluster's
+// histograms and finds the digit for itself, so a digit takes one cluster barrier. Of
+// the tokens equal to the threshold the earliest are taken. The kept tokens' places go
+// to `kept` in order; then the blocks share the kept rows evenly, copy K and V (a 16-byte vector a
+// thread) and replace each place by the token's position. No order of execution
+// shows in the result: counts are integers, places come from prefix sums.
+//
+// The masses are read from memory once (a share of up to 2048 entries stays in shared memory as
+// integers; larger ones are read again for every digit). Few requests get large clusters: one
+// block per (request, head) of an 8-head model would leave the GPU to 8 SMs.
+#include <cooperative_groups.h>
+
 #include "internal.h"
+
+namespace cg = cooperative_groups;
 
 namespace lazyattn {
 
@@ -15,6 +27,13 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kSeg = 2048;                  // entries of a share held in shared memory at a time
+constexpr int kRun = kSeg / kThreads;       // consecutive entries a thread scans
+constexpr int kBits = 11, kBins = 1 << kBits;
+constexpr int kDigits = 3;                  // bits 21..31, 10..20, 0..9
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kKeep = 0xffffffffu;     // key of a sink or a recent token
+constexpr uint32_t kNone = 0xfffffffeu;     // key of a slot without a token (masses end at 0xff800000)
 
 // Order-preserving integer of a mass (larger mass, larger integer): NaN is 0, the
 // least; -0 and 0 are equal.
@@ -24,29 +43,26 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive sums of a block's (a, b) pairs, and the totals. Called by all threads.
-__device__ __forceinline__ int2 block_scan(int2 v, int2 (&warp_sum)[kWarps], int2& total) {
+// Exclusive sum over the block, and the total. Called by all threads.
+__device__ __forceinline__ int block_scan(int v, int (&warp_sum)[kWarps], int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int2 x = v;
+    int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
-        if (lane >= o) {
-            x.x += a;
-            x.y += b;
-        }
+        const int a = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += a;
     }
     __syncthreads();   // the sums of an earlier call have been read
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    int2 before = make_int2(0, 0);
-    total = make_int2(0, 0);
+    int before = 0;
+    total = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) before = total;
-        total.x += warp_sum[w].x;
-        total.y += warp_sum[w].y;
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
     }
-    return make_int2(before.x + x.x - v.x, before.y + x.y - v.y);
+    return before + x - v;
 }
 
 struct EvictParams {
@@ -58,167 +74,332 @@ struct EvictParams {
     int32_t* kept;
     float* dst_mass;
     int32_t budget, sinks, recent;
-    int32_t row_vecs;   // 16-byte vectors of a K or V row
+    int32_t row_shift;   // log2 of the 16-byte vectors of a K or V row
+    int32_t seg;         // entries of a share held at a time (at most kSeg)
 };
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(PoolView pv, EvictParams P) {
-    const int h = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
+struct Shared {
+    int hist[kDigits][kBins];
+    int scan[kWarps];
+    int tokens, bad;           // of this block's share
+    int sure, equal;           // tokens kept for certain, tokens equal to the threshold
+    int digit, want;
+    int warp_sure[kWarps], warp_equal[kWarps];
+};
+
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(PoolView pv, EvictParams P) {
+    extern __shared__ __align__(16) uint32_t dyn[];
+    __shared__ Shared S;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int h = blockIdx.y, r = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hkv = pv.hkv;
     const int e0 = P.entry_offsets[r], E = P.entry_offsets[r + 1] - e0;
     const int d0 = P.dst_offsets[r], DE = P.dst_offsets[r + 1] - d0;
     int32_t* kept = P.kept + ((size_t)r * hkv + h) * P.budget;
-    __shared__ int2 s_sum[kWarps];
-    __shared__ int s_hist[256];
-    __shared__ int s_bad;
-    __shared__ uint32_t s_key;
-    __shared__ int s_need;
-    if (tid == 0) s_bad = 0;
+    const int per = (E + C - 1) / C;
+    const int a0 = min(E, rank * per), a1 = min(E, a0 + per);   // this block's entries
+    const int segs = (a1 - a0 + P.seg - 1) / P.seg;
+    uint32_t* keys = dyn;                                        // [seg][16]
+    int* first = reinterpret_cast<int*>(dyn + (size_t)P.seg * kPage);   // [seg]: tokens before the entry, in the share
+
+    for (int b = tid; b < kDigits * kBins; b += kThreads) (&S.hist[0][0])[b] = 0;
+    if (tid == 0) S.bad = 0;
     __syncthreads();
 
-    // Count the tokens and check the table: pages and positions in range, entries with tokens
-    // ascending in position (each against the last one before it that has tokens).
-    int n_tok = 0;
-    for (int base = 0; base < E; base += kThreads) {
-        const int i = base + tid;
-        const uint64_t e = i < E ? P.entries[e0 + i] : 0ull;
-        const int n = entry_nvalid(e);
-        if (n > 0 && !entry_ok(pv, e)) s_bad = 1;
-        if (n > 0) {
-            for (int k = i - 1; k >= 0; --k) {
-                const uint64_t f = P.entries[e0 + k];
-                if (entry_nvalid(f) == 0) continue;
-                if (entry_start(f) + entry_nvalid(f) > entry_start(e)) s_bad = 1;
-                break;
+    // Count the share's tokens and check the table: pages and positions in range, entries
+    // with tokens ascending in position (each against the last one before it that has tokens).
+    // Leaves the segment's `first`, and the tokens before the segment in `before`.
+    auto load_entries = [&](int seg, int before, bool check) {
+        const int b0 = a0 + seg * P.seg, n_here = min(P.seg, a1 - b0);
+        int n[kRun], sum = 0;
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) {
+            const int i = tid * kRun + j;
+            const uint64_t e = i < n_here ? P.entries[e0 + b0 + i] : 0ull;
+            n[j] = min(entry_nvalid(e), kPage);
+            sum += n[j];
+            if (check && n[j] > 0) {
+                if (!entry_ok(pv, e)) S.bad = 1;
+                for (int k = b0 + i - 1; k >= 0; --k) {
+                    const uint64_t f = P.entries[e0 + k];
+                    if (entry_nvalid(f) == 0) continue;
+                    if (entry_start(f) + entry_nvalid(f) > entry_start(e)) S.bad = 1;
+                    break;
+                }
             }
         }
-        int2 total;
-        block_scan(make_int2(min(n, kPage), 0), s_sum, total);
-        n_tok += total.x;
+        int total;
+        int at = before + block_scan(sum, S.scan, total);
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) {
+            const int i = tid * kRun + j;
+            if (i < n_here) first[i] = at;
+            at += n[j];
+        }
+        __syncthreads();
+        return before + total;
+    };
+    {
+        int tokens = 0;
+        for (int s = 0; s < segs; ++s) tokens = load_entries(s, tokens, true);
+        if (tid == 0) S.tokens = tokens;
+    }
+    cluster.sync();
+    int n_tok = 0, base = 0;
+    bool bad = false;
+    for (int c = 0; c < C; ++c) {
+        const Shared* o = cluster.map_shared_rank(&S, c);
+        if (c < rank) base += o->tokens;
+        n_tok += o->tokens;
+        bad = bad || o->bad != 0;
     }
     const int count = min(n_tok, P.budget);
     const int pages = (count + kPage - 1) / kPage;
-    if (tid == 0 && (DE < pages || DE > (LAZYATTN_MAX_START + 1) / kPage)) s_bad = 1;
+    bad = bad || DE < pages || DE > (LAZYATTN_MAX_START + 1) / kPage;
+    int dst_bad = 0;
     for (int i = tid; i < min(DE, pages); i += kThreads)
-        if ((uint32_t)P.dst_entries[d0 + i] >= (uint32_t)pv.num_pages) s_bad = 1;
-    __syncthreads();
-    const bool bad = s_bad != 0;
+        dst_bad |= (uint32_t)P.dst_entries[d0 + i] >= (uint32_t)pv.num_pages;
+    bad = __syncthreads_or(dst_bad) != 0 || bad;
     if (bad && tid == 0) record_error(pv.status, LAZYATTN_ERANGE);
     const int cnt = bad ? 0 : count;
 
-    // New entries: the upper word holds start, count and the writable bit.
-    if (h == 0)
+    // New entries: the upper word holds start, count and the writable bit (blocks of other
+    // heads read the lower word, the page, meanwhile).
+    if (h == 0 && rank == 0)
         for (int i = tid; i < DE; i += kThreads) {
             uint32_t* hi = reinterpret_cast<uint32_t*>(P.dst_entries + d0 + i) + 1;
             const uint32_t start = (uint32_t)min((int64_t)i * kPage, (int64_t)LAZYATTN_MAX_START);
             *hi = (*hi & 0x80000000u) | start | ((uint32_t)max(0, min(kPage, cnt - i * kPage)) << 26);
         }
 
-    auto mass_at = [&](int i, int s) { return P.mass[((size_t)(e0 + i) * hkv + h) * kPage + s]; };
     const int lo = min(P.sinks, n_tok), hi = max(lo, n_tok - P.recent);   // tokens [lo, hi) compete
-    const int need = cnt - (n_tok - (hi - lo));                          // of them this many stay
     const bool all = cnt == n_tok;
-    uint32_t key = 0;       // the smallest kept mass
+    // The segment's keys: thread = (entry, 4 slots).
+    auto load_keys = [&](int seg) {
+        const int b0 = a0 + seg * P.seg, n_here = min(P.seg, a1 - b0);
+        for (int x = tid; x < n_here * 4; x += kThreads) {
+            const int i = x >> 2, s0 = (x & 3) * 4;
+            const int n = min(entry_nvalid(P.entries[e0 + b0 + i]), kPage);
+            const float4 m = *reinterpret_cast<const float4*>(P.mass + ((size_t)(e0 + b0 + i) * hkv + h) * kPage + s0);
+            const int t = base + first[i] + s0;
+            auto key = [&](float v, int j) {
+                if (s0 + j >= n) return kNone;
+                return all || t + j < lo || t + j >= hi ? kKeep : mass_key(v);
+            };
+            *reinterpret_cast<uint4*>(keys + x * 4) = make_uint4(key(m.x, 0), key(m.y, 1), key(m.z, 2), key(m.w, 3));
+        }
+        __syncthreads();
+    };
+    // Run f(slots) over the share with each segment's keys in place.
+    auto each_segment = [&](auto f) {
+        int before = 0;
+        for (int s = 0; s < segs; ++s) {
+            if (segs > 1) {
+                __syncthreads();
+                before = load_entries(s, before, false);
+                load_keys(s);
+            }
+            f(min(P.seg, a1 - (a0 + s * P.seg)) * kPage);
+        }
+    };
+    if (!bad && segs == 1) load_keys(0);
+
+    uint32_t key = kNone;   // the smallest competing mass that stays (kNone: none does)
     int equal = 0;          // how many tokens equal to it stay
-    if (!bad && !all) {
-        int want = need;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int b = tid; b < 256; b += kThreads) s_hist[b] = 0;
-            __syncthreads();
-            int at = 0;
-            for (int base = 0; base < E; base += kThreads) {
-                const int i = base + tid;
-                const int n = i < E ? entry_nvalid(P.entries[e0 + i]) : 0;
-                int2 total;
-                const int first = at + block_scan(make_int2(n, 0), s_sum, total).x;
-                at += total.x;
-                for (int s = 0; s < n; ++s) {
-                    const int t = first + s;
-                    if (t < lo || t >= hi) continue;
-                    const uint32_t k = mass_key(mass_at(i, s));
-                    if (shift == 24 || (k >> (shift + 8)) == (key >> (shift + 8))) atomicAdd(&s_hist[(k >> shift) & 255], 1);
+    int want = cnt - (n_tok - (hi - lo));   // of the competing tokens this many stay
+    if (!bad && !all && want > 0) {
+        key = 0;
+#pragma unroll 1
+        for (int dg = 0; dg < kDigits; ++dg) {
+            const int shift = dg == 0 ? 21 : dg == 1 ? 10 : 0, bins = dg == 2 ? 1 << 10 : kBins;
+            const uint32_t above = dg == 0 ? 0u : 0xffffffffu << (dg == 1 ? 21 : 10);   // the bits found so far
+            each_segment([&](int slots) {
+                for (int x = tid; x < slots; x += kThreads) {
+                    const uint32_t k = keys[x];
+                    if (k < kNone && (k & above) == key) atomicAdd(&S.hist[dg][(k >> shift) & (bins - 1)], 1);
                 }
+            });
+            cluster.sync();
+            // thread t has the bins 4 (511 - t) .. + 3, so that sums run from the largest masses down
+            const int b0 = 4 * (kThreads - 1 - tid);
+            int c4[4] = {0, 0, 0, 0};
+            for (int c = 0; c < C; ++c) {
+                const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&S, c)->hist[dg] + b0);
+                c4[0] += v.x; c4[1] += v.y; c4[2] += v.z; c4[3] += v.w;
+            }
+            int total;
+            int seen = block_scan(c4[0] + c4[1] + c4[2] + c4[3], S.scan, total);
+#pragma unroll
+            for (int j = 3; j >= 0; --j) {
+                if (seen < want && want <= seen + c4[j]) {   // one thread, one bin
+                    S.digit = b0 + j;
+                    S.want = want - seen;
+                }
+                seen += c4[j];
             }
             __syncthreads();
-            if (tid == 0) {
-                int above = 0, b = 255;
-                for (; b > 0 && above + s_hist[b] < want; --b) above += s_hist[b];
-                s_key = key | ((uint32_t)b << shift);
-                s_need = want - above;
-            }
+            key |= (uint32_t)S.digit << shift;
+            want = S.want;
             __syncthreads();
-            key = s_key;
-            want = s_need;
         }
         equal = want;
     }
 
-    // Places of the kept tokens, in table order.
-    if (!bad) {
-        int at = 0, at_eq = 0, at_kept = 0;
-        for (int base = 0; base < E; base += kThreads) {
-            const int i = base + tid;
-            const int n = i < E ? entry_nvalid(P.entries[e0 + i]) : 0;
-            int2 total;
-            const int first = at + block_scan(make_int2(n, 0), s_sum, total).x;
-            at += total.x;
-            uint32_t gt = 0, eq = 0;   // slots kept for sure; slots equal to the threshold
-            for (int s = 0; s < n; ++s) {
-                const int t = first + s;
-                if (all || t < lo || t >= hi) {
-                    gt |= 1u << s;
-                } else {
-                    const uint32_t k = mass_key(mass_at(i, s));
-                    if (k > key) gt |= 1u << s;
-                    if (k == key) eq |= 1u << s;
-                }
-            }
-            const int eq_before = at_eq + block_scan(make_int2(__popc(eq), 0), s_sum, total).x;
-            at_eq += total.x;
-            int take = max(0, min(__popc(eq), equal - eq_before));
-            for (uint32_t todo = eq; take > 0; todo &= todo - 1, --take) gt |= todo & -todo;
-            int to = at_kept + block_scan(make_int2(__popc(gt), 0), s_sum, total).x;
-            at_kept += total.x;
-            for (uint32_t todo = gt; todo; todo &= todo - 1, ++to) kept[to] = i * kPage + __ffs(todo) - 1;
+    // A warp's contiguous part of a segment, 32 slots at a time: f(slot, kept for certain, equal to the threshold).
+    auto each_slot = [&](int slots, auto f) {
+        const int part = ((slots + 31) / 32 + kWarps - 1) / kWarps * 32;
+        for (int x0 = warp * part; x0 < min(slots, (warp + 1) * part); x0 += 32) {
+            const uint32_t k = x0 + lane < slots ? keys[x0 + lane] : kNone;
+            f(x0 + lane, k == kKeep || (k < kNone && k > key), k < kNone && k == key);
         }
+    };
+    int sure = 0, same = 0;   // the warp's counts over the whole share
+    if (!bad)
+        each_segment([&](int slots) {
+            each_slot(slots, [&](int, bool s, bool e) {
+                sure += __popc(__ballot_sync(0xffffffffu, s));
+                same += __popc(__ballot_sync(0xffffffffu, e));
+            });
+        });
+    if (lane == 0) {
+        S.warp_sure[warp] = sure;
+        S.warp_equal[warp] = same;
     }
     __syncthreads();
+    if (tid == 0) {
+        int s = 0, e = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            s += S.warp_sure[w];
+            e += S.warp_equal[w];
+        }
+        S.sure = s;
+        S.equal = e;
+    }
+    cluster.sync();
+    int sure0 = 0, same0 = 0;   // tokens before this block's share (then: before the segment)
+    for (int c = 0; c < rank; ++c) {
+        const Shared* o = cluster.map_shared_rank(&S, c);
+        sure0 += o->sure;
+        same0 += o->equal;
+    }
+    // Places of the kept tokens, in table order. Of `same` tokens equal to the threshold the first
+    // `equal` are kept, so the place of a token is (sure before) + min(equal, same before).
+    if (!bad) {
+        int at = 0;   // entries of the share before the segment
+        each_segment([&](int slots) {
+            if (segs > 1) {   // the warps' counts of this segment
+                int s = 0, e = 0;
+                each_slot(slots, [&](int, bool a, bool b) {
+                    s += __popc(__ballot_sync(0xffffffffu, a));
+                    e += __popc(__ballot_sync(0xffffffffu, b));
+                });
+                if (lane == 0) {
+                    S.warp_sure[warp] = s;
+                    S.warp_equal[warp] = e;
+                }
+                __syncthreads();
+            }
+            int s_at = sure0, e_at = same0;
+            for (int w = 0; w < kWarps; ++w) {
+                const int s = S.warp_sure[w], e = S.warp_equal[w];
+                if (w < warp) {
+                    s_at += s;
+                    e_at += e;
+                }
+                sure0 += s;
+                same0 += e;
+            }
+            each_slot(slots, [&](int x, bool s, bool e) {
+                const unsigned below = (1u << lane) - 1u;
+                const unsigned sb = __ballot_sync(0xffffffffu, s), eb = __ballot_sync(0xffffffffu, e);
+                const int e_here = e_at + __popc(eb & below);
+                if (s || (e && e_here < equal))
+                    kept[s_at + __popc(sb & below) + min(equal, e_here)] = (a0 + at) * kPage + x;
+                s_at += __popc(sb);
+                e_at += __popc(eb);
+            });
+            at += P.seg;
+        });
+    }
+    __threadfence();
+    cluster.sync();   // the cluster's places are written (and no shared memory of another block is read from here on)
 
-    // Copy: `vecs` threads per token; slots of the last page past the tokens become zeros.
-    const int vecs = P.row_vecs, per = kThreads / vecs, v = tid % vecs;
+    // Copy: a row's vectors are consecutive threads of a warp; the blocks take equal shares of the
+    // new rows. Slots of the last page past the tokens become zeros.
+    const int vecs = 1 << P.row_shift, rows = kThreads >> P.row_shift, v = tid & (vecs - 1);
     uint4* kp = static_cast<uint4*>(pv.k_pool);
     uint4* vp = static_cast<uint4*>(pv.v_pool);
     const int used = (cnt + kPage - 1) / kPage * kPage;
-    for (int j = tid / vecs; j < used; j += per) {
-        const uint32_t page = (uint32_t)P.dst_entries[d0 + j / kPage];
-        const size_t dst = (((size_t)page * hkv + h) * kPage + j % kPage) * vecs + v;
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (j < cnt) {
-            const int code = kept[j];
-            const uint64_t e = P.entries[e0 + code / kPage];
-            const size_t src = (((size_t)entry_page(e) * hkv + h) * kPage + code % kPage) * vecs + v;
-            a = kp[src];
-            b = vp[src];
-            if (v == 0 && P.dst_mass)
-                P.dst_mass[((size_t)(d0 + j / kPage) * hkv + h) * kPage + j % kPage] = mass_at(code / kPage, code % kPage);
-        } else if (v == 0 && P.dst_mass) {
-            P.dst_mass[((size_t)(d0 + j / kPage) * hkv + h) * kPage + j % kPage] = 0.f;
+    const int share = ((used + C - 1) / C + rows - 1) / rows * rows;
+    const int j_end = min(used, (rank + 1) * share);
+    constexpr int kAhead = 4;   // rows in flight per thread
+    for (int jb = rank * share + (tid >> P.row_shift); jb < j_end; jb += rows * kAhead) {
+        uint4 a[kAhead], b[kAhead];
+        float m[kAhead];
+        int pos[kAhead];
+        size_t dst[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int j = jb + u * rows;
+            a[u] = b[u] = make_uint4(0, 0, 0, 0);
+            m[u] = 0.f;
+            pos[u] = -1;
+            if (j < j_end) {
+                dst[u] = (((size_t)(uint32_t)P.dst_entries[d0 + j / kPage] * hkv + h) * kPage + j % kPage) * vecs + v;
+                if (j < cnt) {
+                    const int code = kept[j];
+                    const uint64_t e = P.entries[e0 + code / kPage];
+                    const size_t src = (((size_t)entry_page(e) * hkv + h) * kPage + code % kPage) * vecs + v;
+                    a[u] = kp[src];
+                    b[u] = vp[src];
+                    pos[u] = entry_start(e) + code % kPage;
+                    if (P.dst_mass) m[u] = P.mass[((size_t)(e0 + code / kPage) * hkv + h) * kPage + code % kPage];
+                }
+            }
         }
-        kp[dst] = a;
-        vp[dst] = b;
+        __syncwarp();   // the row's threads have read its place
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int j = jb + u * rows;
+            if (j >= j_end) continue;
+            kp[dst[u]] = a[u];
+            vp[dst[u]] = b[u];
+            if (v == 0) {
+                if (j < cnt) kept[j] = pos[u];
+                if (P.dst_mass) P.dst_mass[((size_t)(d0 + j / kPage) * hkv + h) * kPage + j % kPage] = m[u];
+            }
+        }
     }
-    __syncthreads();
-    for (int j = tid; j < P.budget; j += kThreads)
-        kept[j] = j < cnt ? entry_start(P.entries[e0 + kept[j] / kPage]) + kept[j] % kPage : -1;
+    for (int j = cnt + rank * kThreads + tid; j < P.budget; j += C * kThreads) kept[j] = -1;
     if (P.dst_mass)
-        for (int j = used + tid; j < DE * kPage; j += kThreads)
+        for (int j = used + rank * kThreads + tid; j < DE * kPage; j += C * kThreads)
             P.dst_mass[((size_t)(d0 + j / kPage) * hkv + h) * kPage + j % kPage] = 0.f;
 }
 
 }  // namespace
 
+// Blocks per (request, KV head): as many as give the GPU about two blocks a SM, at least
+// as many as hold the table's keys in shared memory (up to eight).
+static int evict_cluster(const lazyattn_pool& p, const lazyattn_batch& b) {
+    const int64_t items = (int64_t)b.num_requests * p.d.n_kv_heads;
+    int c = 1;
+    while (c < kMaxCluster && (items * c < 2 * (int64_t)p.sm_count || (int64_t)b.max_entries > (int64_t)c * kSeg)) c *= 2;
+    return c;
+}
+
+static int evict_smem(int seg) { return seg * (kPage * (int)sizeof(uint32_t) + (int)sizeof(int)); }
+
+int evict_init() {
+    return cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, evict_smem(kSeg)) == cudaSuccess
+               ? LAZYATTN_OK
+               : LAZYATTN_ECUDA;
+}
+
 int launch_evict(const lazyattn_pool& p, const lazyattn_batch& b, const float* mass, int32_t budget, int32_t sinks,
                  int32_t recent, uint64_t* dst_entries, const int32_t* dst_offsets, int32_t* kept, float* dst_mass,
                  cudaStream_t stream) {
+    const int C = evict_cluster(p, b);
     EvictParams P;
     P.entries = b.entries;
     P.entry_offsets = b.entry_offsets;
@@ -230,8 +411,22 @@ int launch_evict(const lazyattn_pool& p, const lazyattn_batch& b, const float* m
     P.budget = budget;
     P.sinks = sinks;
     P.recent = recent;
-    P.row_vecs = p.d.head_dim * (p.d.dtype == LAZYATTN_F32 ? 4 : 2) / 16;
-    evict_kernel<<<dim3(p.d.n_kv_heads, b.num_requests), kThreads, 0, stream>>>(p.view(), P);
+    P.row_shift = 0;
+    while ((16 << P.row_shift) < p.d.head_dim * (p.d.dtype == LAZYATTN_F32 ? 4 : 2)) ++P.row_shift;
+    P.seg = std::min(kSeg, std::max(1, (b.max_entries + C - 1) / C));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C, p.d.n_kv_heads, b.num_requests);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = evict_smem(P.seg);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, evict_kernel, p.view(), P) != cudaSuccess) return LAZYATTN_ECUDA;
     return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;
 }
 

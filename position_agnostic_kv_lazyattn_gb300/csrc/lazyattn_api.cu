@@ -171,6 +171,10 @@ int lazyattn_pool_create(const lazyattn_pool_desc* desc, void* stream, lazyattn_
         delete p;
         return LAZYATTN_ECUDA;
     }
+    if (evict_init() != LAZYATTN_OK) {
+        delete p;
+        return LAZYATTN_ECUDA;
+    }
     p->decode_slots = p->sm_count * std::max(occ, 1);
     if (d.dtype == LAZYATTN_BF16 && !encode_pool_maps(*p)) {
         delete p;

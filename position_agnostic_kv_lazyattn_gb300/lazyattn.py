@@ -155,7 +155,7 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())   # a tenth of current_stream()'s cost
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
