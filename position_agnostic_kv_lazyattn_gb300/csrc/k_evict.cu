@@ -8,9 +8,10 @@
 // into a histogram in shared memory, and every block reads all the cluster's
 // histograms and finds the digit for itself, so a digit takes one cluster barrier. Of
 // the tokens equal to the threshold the earliest are taken. The kept tokens' places go
-// to `kept` in order; then the blocks share the kept rows evenly, copy K and V (a 16-byte vector a
-// thread) and replace each place by the token's position. No order of execution
-// shows in the result: counts are integers, places come from prefix sums.
+// to `kept` in order. No order of execution shows in the result: counts are integers,
+// places come from prefix sums. A second kernel copies the rows, which is all of
+// the memory traffic that counts, over the whole GPU (in the selecting blocks, each wave's
+// copies waited for its selection: 32 requests cut to 2048 tokens took 156 us).
 //
 // The masses are read from memory once (a share of up to 2048 entries stays in shared memory as
 // integers; larger ones are read again for every digit). Few requests get large clusters: one
@@ -74,7 +75,6 @@ struct EvictParams {
     int32_t* kept;
     float* dst_mass;
     int32_t budget, sinks, recent;
-    int32_t row_shift;   // log2 of the 16-byte vectors of a K or V row
     int32_t seg;         // entries of a share held at a time (at most kSeg)
 };
 
@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(PoolView pv, EvictPa
     // The segment's keys: thread = (entry, 4 slots).
     auto load_keys = [&](int seg) {
         const int b0 = a0 + seg * P.seg, n_here = min(P.seg, a1 - b0);
+#pragma unroll 4
         for (int x = tid; x < n_here * 4; x += kThreads) {
             const int i = x >> 2, s0 = (x & 3) * 4;
             const int n = min(entry_nvalid(P.entries[e0 + b0 + i]), kPage);
@@ -215,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(PoolView pv, EvictPa
             const int shift = dg == 0 ? 21 : dg == 1 ? 10 : 0, bins = dg == 2 ? 1 << 10 : kBins;
             const uint32_t above = dg == 0 ? 0u : 0xffffffffu << (dg == 1 ? 21 : 10);   // the bits found so far
             each_segment([&](int slots) {
+#pragma unroll 4
                 for (int x = tid; x < slots; x += kThreads) {
                     const uint32_t k = keys[x];
                     if (k < kNone && (k & above) == key) atomicAdd(&S.hist[dg][(k >> shift) & (bins - 1)], 1);
@@ -322,69 +324,63 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(PoolView pv, EvictPa
             at += P.seg;
         });
     }
-    __threadfence();
-    cluster.sync();   // the cluster's places are written (and no shared memory of another block is read from here on)
-
-    // Copy: a row's vectors are consecutive threads of a warp; the blocks take equal shares of the
-    // new rows. Slots of the last page past the tokens become zeros.
-    const int vecs = 1 << P.row_shift, rows = kThreads >> P.row_shift, v = tid & (vecs - 1);
-    uint4* kp = static_cast<uint4*>(pv.k_pool);
-    uint4* vp = static_cast<uint4*>(pv.v_pool);
-    const int used = (cnt + kPage - 1) / kPage * kPage;
-    const int share = ((used + C - 1) / C + rows - 1) / rows * rows;
-    const int j_end = min(used, (rank + 1) * share);
-    constexpr int kAhead = 4;   // rows in flight per thread
-    for (int jb = rank * share + (tid >> P.row_shift); jb < j_end; jb += rows * kAhead) {
-        uint4 a[kAhead], b[kAhead];
-        float m[kAhead];
-        int pos[kAhead];
-        size_t dst[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int j = jb + u * rows;
-            a[u] = b[u] = make_uint4(0, 0, 0, 0);
-            m[u] = 0.f;
-            pos[u] = -1;
-            if (j < j_end) {
-                dst[u] = (((size_t)(uint32_t)P.dst_entries[d0 + j / kPage] * hkv + h) * kPage + j % kPage) * vecs + v;
-                if (j < cnt) {
-                    const int code = kept[j];
-                    const uint64_t e = P.entries[e0 + code / kPage];
-                    const size_t src = (((size_t)entry_page(e) * hkv + h) * kPage + code % kPage) * vecs + v;
-                    a[u] = kp[src];
-                    b[u] = vp[src];
-                    pos[u] = entry_start(e) + code % kPage;
-                    if (P.dst_mass) m[u] = P.mass[((size_t)(e0 + code / kPage) * hkv + h) * kPage + code % kPage];
-                }
-            }
-        }
-        __syncwarp();   // the row's threads have read its place
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int j = jb + u * rows;
-            if (j >= j_end) continue;
-            kp[dst[u]] = a[u];
-            vp[dst[u]] = b[u];
-            if (v == 0) {
-                if (j < cnt) kept[j] = pos[u];
-                if (P.dst_mass) P.dst_mass[((size_t)(d0 + j / kPage) * hkv + h) * kPage + j % kPage] = m[u];
-            }
-        }
-    }
     for (int j = cnt + rank * kThreads + tid; j < P.budget; j += C * kThreads) kept[j] = -1;
+    const int used = (cnt + kPage - 1) / kPage * kPage;
     if (P.dst_mass)
         for (int j = used + rank * kThreads + tid; j < DE * kPage; j += C * kThreads)
             P.dst_mass[((size_t)(d0 + j / kPage) * hkv + h) * kPage + j % kPage] = 0.f;
+    cluster.sync();   // no block leaves while another reads its shared memory
+}
+
+// Block = (kept rows, KV head, request). A row's 16-byte vectors are consecutive threads of a
+// warp; a place becomes the token's position once the block has read it. Slots of the
+// last page past the tokens become zeros. One row a thread: more rows in flight per thread cost
+// warps, which hide the three dependent loads better (32 requests cut to 2048 tokens, both kernels:
+// 115 us; two rows 121, four 134, eight 244).
+constexpr int kCopyThreads = 256;
+template <int VECS>
+__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(PoolView pv, EvictParams P) {
+    constexpr int kRows = kCopyThreads / VECS;
+    const int h = blockIdx.y, r = blockIdx.z, hkv = pv.hkv;
+    const int v = threadIdx.x % VECS, j = (int)blockIdx.x * kRows + (int)threadIdx.x / VECS;
+    const int e0 = P.entry_offsets[r], d0 = P.dst_offsets[r];
+    int32_t* kept = P.kept + ((size_t)r * hkv + h) * P.budget;
+    uint4* kp = static_cast<uint4*>(pv.k_pool);
+    uint4* vp = static_cast<uint4*>(pv.v_pool);
+    grid_dep_wait();
+    const int j16 = j / kPage * kPage;
+    const int code = j < P.budget ? kept[j] : -1;
+    const bool page = j16 < P.budget && kept[j16] >= 0;   // the row's page holds a kept token (place or position)
+    __syncthreads();
+    if (!page) return;
+    const size_t slot = (size_t)j % kPage;
+    const size_t dst = (((size_t)(uint32_t)P.dst_entries[d0 + j / kPage] * hkv + h) * kPage + slot) * VECS + v;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    float m = 0.f;
+    if (code >= 0) {
+        const uint64_t e = P.entries[e0 + code / kPage];
+        const size_t src = (((size_t)entry_page(e) * hkv + h) * kPage + code % kPage) * VECS + v;
+        a = kp[src];
+        b = vp[src];
+        if (v == 0) {
+            if (P.dst_mass) m = P.mass[((size_t)(e0 + code / kPage) * hkv + h) * kPage + code % kPage];
+            kept[j] = entry_start(e) + code % kPage;
+        }
+    }
+    kp[dst] = a;
+    vp[dst] = b;
+    if (v == 0 && P.dst_mass) P.dst_mass[((size_t)(d0 + j / kPage) * hkv + h) * kPage + slot] = m;
 }
 
 }  // namespace
 
-// Blocks per (request, KV head): as many as give the GPU about two blocks a SM, at least
-// as many as hold the table's keys in shared memory (up to eight).
+// Blocks per (request, KV head). The phases are bound by their barriers and latencies, so
+// blocks are few: one per 1024 entries (16 K tokens), or per 512 while all blocks fit the GPU
+// at once (one request of 50,000 tokens: 24 us against 29; four: 48 against 39).
 static int evict_cluster(const lazyattn_pool& p, const lazyattn_batch& b) {
     const int64_t items = (int64_t)b.num_requests * p.d.n_kv_heads;
     int c = 1;
-    while (c < kMaxCluster && (items * c < 2 * (int64_t)p.sm_count || (int64_t)b.max_entries > (int64_t)c * kSeg)) c *= 2;
+    while (c < kMaxCluster && (b.max_entries > c * 1024 || (b.max_entries > c * 512 && items * 2 * c <= p.sm_count))) c *= 2;
     return c;
 }
 
@@ -411,8 +407,6 @@ int launch_evict(const lazyattn_pool& p, const lazyattn_batch& b, const float* m
     P.budget = budget;
     P.sinks = sinks;
     P.recent = recent;
-    P.row_shift = 0;
-    while ((16 << P.row_shift) < p.d.head_dim * (p.d.dtype == LAZYATTN_F32 ? 4 : 2)) ++P.row_shift;
     P.seg = std::min(kSeg, std::max(1, (b.max_entries + C - 1) / C));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C, p.d.n_kv_heads, b.num_requests);
@@ -427,6 +421,12 @@ int launch_evict(const lazyattn_pool& p, const lazyattn_batch& b, const float* m
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, evict_kernel, p.view(), P) != cudaSuccess) return LAZYATTN_ECUDA;
+    const bool wide = p.d.head_dim * (p.d.dtype == LAZYATTN_F32 ? 4 : 2) == 512;   // 16-byte vectors a row: 32, else 16
+    const int rows = kCopyThreads / (wide ? 32 : 16);
+    if (launch_dependent(wide ? evict_copy_kernel<32> : evict_copy_kernel<16>,
+                         dim3((unsigned)(((int64_t)budget + rows - 1) / rows), p.d.n_kv_heads, b.num_requests),
+                         dim3(kCopyThreads), 0, stream, p.view(), P) != cudaSuccess)
+        return LAZYATTN_ECUDA;
     return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;
 }
 

@@ -159,12 +159,22 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_DTYPE_NAMES = {}   # torch dtype -> its name, filled on use (torch is not imported here)
+
+
 def _dense(where: str, *tensors, dtype=None):
     """Refuse tensors whose elements are not laid out densely (the C ABI takes plain
     pointers) or, where dtype names are given, are of another type."""
     for t in tensors:
-        if hasattr(t, "is_contiguous") and (not t.is_contiguous() or
-                                            (dtype and str(t.dtype).split(".")[-1] not in dtype)):
+        if not hasattr(t, "is_contiguous"):   # None, or a plain address
+            continue
+        ok = t.is_contiguous()
+        if ok and dtype:
+            name = _DTYPE_NAMES.get(t.dtype)
+            if name is None:
+                name = _DTYPE_NAMES[t.dtype] = str(t.dtype).split(".")[-1]
+            ok = name in dtype
+        if not ok:
             raise LazyAttnError(LAZYATTN_EINVAL, f"{where}: needs a contiguous tensor" +
                                 (f" of {' or '.join(dtype)}" if dtype else ""))
 
