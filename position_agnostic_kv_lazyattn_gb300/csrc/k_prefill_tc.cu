@@ -745,60 +745,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             row_valid = false;
         }
 
-        // Q row: rotate at m_row, scale by log2(e) times the pool's logit scale (1/sqrt(D)),
-        // fp16, 128B-swizzled K-major
+        // Q: rotated at the row's position, scaled by log2(e) times the pool's logit scale
+        // (1/sqrt(D)), fp16, 128B-swizzled K-major. Eight lanes take a row (lane u: dims 8u.. of both
+        // halves), four rows at a time: a load then touches four lines, not a line per lane. (A
+        // thread per row kept the load units busy for most of 7 us, and the producer's first
+        // block-table read waited behind them.)
         {
             uint8_t* qsm = sm + kOffQ + qi * kQBytes;
             const float sc = kLog2e * pv.qk_scale;
-            const __nv_bfloat16* qp_ = P.q + ((size_t)(q0 + tok) * Hq + (size_t)h * g + jh) * kD;
-            const float* cs = reinterpret_cast<const float*>(pv.rope + (size_t)(row_valid ? m_row : 0) * (kD / 2));
-            // The row's position-table line (512 B) is fetched into L1 while the
-            // q words load; each half of the row's dims loads its q words together.
-            if (!ALIBI && row_valid) {
+            const int u = lane & 7;
+#pragma unroll 2
+            for (int step = 0; step < 8; ++step) {
+                const int tr = 32 * quarter + 4 * step + (lane >> 3), crow = qi * kTileM + tr;
+                const int tl_ = crow / g, m = qs + i0 + tl_;
+                const bool valid = tl_ < ntok && m >= 0 && m < pv.max_position;
+                uint4 w1 = make_uint4(0, 0, 0, 0), w2 = w1;
+                if (valid) {
+                    const __nv_bfloat16* qp_ = P.q + ((size_t)(q0 + i0 + tl_) * Hq + (size_t)h * g + crow - tl_ * g) * kD;
+                    uint4 a = __ldg(reinterpret_cast<const uint4*>(qp_ + (INTER ? 16 * u : 8 * u)));
+                    uint4 b = __ldg(reinterpret_cast<const uint4*>(qp_ + (INTER ? 16 * u + 8 : 64 + 8 * u)));
+                    const float4* c4 = reinterpret_cast<const float4*>(pv.rope + (size_t)m * (kD / 2)) + 4 * u;
+                    float4 f[4];
 #pragma unroll
-                for (int l = 0; l < 4; ++l) asm volatile("prefetch.global.L1 [%0];" ::"l"(cs + 32 * l));
-            }
-#pragma unroll 1
-            for (int h4 = 0; h4 < 2; ++h4) {
-                uint4 qa[4], qb[4];
+                    for (int v = 0; v < 4; ++v) f[v] = ALIBI ? make_float4(1.f, 0.f, 1.f, 0.f) : __ldg(c4 + v);
+                    float x1[8], x2[8];
+                    if (INTER) deinterleave16(a, b, a, b);
+                    unpack8(a, x1);
+                    unpack8(b, x2);
+                    float n2 = 0.f;   // input range: rotated, scaled pairs must stay finite in fp16
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int u = 4 * h4 + i;
-                    qa[i] = row_valid ? __ldg(reinterpret_cast<const uint4*>(qp_ + (INTER ? 16 * u : 8 * u)))
-                                      : make_uint4(0, 0, 0, 0);
-                    qb[i] = row_valid ? __ldg(reinterpret_cast<const uint4*>(qp_ + (INTER ? 16 * u + 8 : 64 + 8 * u)))
-                                      : make_uint4(0, 0, 0, 0);
-                }
+                    for (int v = 0; v < 8; ++v) n2 = fmaxf(n2, fmaf(x1[v], x1[v], x2[v] * x2[v]));
+                    if (!(n2 * sc * sc <= kMaxPairNorm2)) record_error(pv.status, LAZYATTN_ERANGE);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int u = 4 * h4 + i;
-                    uint4 w1 = make_uint4(0, 0, 0, 0), w2 = w1;
-                    if (row_valid) {
-                        float x1[8], x2[8];
-                        uint4 a = qa[i], b = qb[i];
-                        if (INTER) deinterleave16(a, b, a, b);
-                        unpack8(a, x1);
-                        unpack8(b, x2);
-                        float n2 = 0.f;   // input range: rotated, scaled pairs must stay finite in fp16
-#pragma unroll
-                        for (int v = 0; v < 8; ++v) n2 = fmaxf(n2, fmaf(x1[v], x1[v], x2[v] * x2[v]));
-                        if (!(n2 * sc * sc <= kMaxPairNorm2)) record_error(pv.status, LAZYATTN_ERANGE);
-                        const float4* c4 = reinterpret_cast<const float4*>(cs + 16 * u);
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const float4 f = ALIBI ? make_float4(1.f, 0.f, 1.f, 0.f) : __ldg(c4 + v);
-                            const float a0 = x1[2 * v], z0 = x2[2 * v], a1 = x1[2 * v + 1], z1 = x2[2 * v + 1];
-                            x1[2 * v] = (a0 * f.x - z0 * f.y) * sc;
-                            x2[2 * v] = (a0 * f.y + z0 * f.x) * sc;
-                            x1[2 * v + 1] = (a1 * f.z - z1 * f.w) * sc;
-                            x2[2 * v + 1] = (a1 * f.w + z1 * f.z) * sc;
-                        }
-                        w1 = pack8_h(x1);
-                        w2 = pack8_h(x2);
+                    for (int v = 0; v < 4; ++v) {
+                        const float a0 = x1[2 * v], z0 = x2[2 * v], a1 = x1[2 * v + 1], z1 = x2[2 * v + 1];
+                        x1[2 * v] = (a0 * f[v].x - z0 * f[v].y) * sc;
+                        x2[2 * v] = (a0 * f[v].y + z0 * f[v].x) * sc;
+                        x1[2 * v + 1] = (a1 * f[v].z - z1 * f[v].w) * sc;
+                        x2[2 * v + 1] = (a1 * f[v].w + z1 * f[v].z) * sc;
                     }
-                    *reinterpret_cast<uint4*>(qsm + sw128_offset(trow, u)) = w1;
-                    *reinterpret_cast<uint4*>(qsm + kQChunk + sw128_offset(trow, u)) = w2;
+                    w1 = pack8_h(x1);
+                    w2 = pack8_h(x2);
                 }
+                *reinterpret_cast<uint4*>(qsm + sw128_offset(tr, u)) = w1;
+                *reinterpret_cast<uint4*>(qsm + kQChunk + sw128_offset(tr, u)) = w2;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -983,8 +973,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (active) {
             if (ok && k >= 1) ok = mbar_wait(smem_u32(&bar_odone[qi]), (k - 1) & 1, abort_flag);
             tc_fence_after();
-            __nv_bfloat16* op = P.out + ((size_t)(q0 + tok) * Hq + (size_t)h * g + jh) * kD;
+            // Rows go through this warp's 8 KB of its Q tile (whose last QK is done), 16-byte units
+            // XORed with the row, so that the stores to memory are whole rows: two a store, not a
+            // line per lane.
             const float inv = (ok && l_run > 0.f) ? 1.f / l_run : 0.f;
+            uint8_t* stage = sm + kOffQ + qi * kQBytes + quarter * 32 * 256;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t v[32];
@@ -994,15 +987,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
-                if (t_local < ntok) {
-                    uint4* dst = reinterpret_cast<uint4*>(op + 32 * c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float* f = reinterpret_cast<const float*>(v + 8 * i);
-                        dst[i] = make_uint4(pack_bf2(f[0] * inv, f[1] * inv), pack_bf2(f[2] * inv, f[3] * inv),
-                                            pack_bf2(f[4] * inv, f[5] * inv), pack_bf2(f[6] * inv, f[7] * inv));
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const float* f = reinterpret_cast<const float*>(v + 8 * i);
+                    *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * c + i) ^ (lane & 7)) << 4)) =
+                        make_uint4(pack_bf2(f[0] * inv, f[1] * inv), pack_bf2(f[2] * inv, f[3] * inv),
+                                   pack_bf2(f[4] * inv, f[5] * inv), pack_bf2(f[6] * inv, f[7] * inv));
                 }
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int rr = 2 * i + (lane >> 4), crow = qi * kTileM + 32 * quarter + rr, tl_ = crow / g;
+                if (tl_ < ntok)
+                    reinterpret_cast<uint4*>(P.out + ((size_t)(q0 + i0 + tl_) * Hq + (size_t)h * g + crow - tl_ * g) *
+                                                         kD)[lane & 15] =
+                        *reinterpret_cast<const uint4*>(stage + rr * 256 + (((lane & 15) ^ (rr & 7)) << 4));
             }
         }
     }
