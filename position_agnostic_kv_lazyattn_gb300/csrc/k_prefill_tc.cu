@@ -736,7 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t ts = tl + qi * 128;         // S_i, and P_i over its first 64 columns
         const uint32_t to = tl + 256 + qi * 128;   // O_i
-        const int t_local = row / g, jh = row - t_local * g;
+        const int lg = 31 - __clz(g);              // g divides 256 and is at most 8: a power of two
+        const int t_local = row >> lg, jh = row - t_local * g;
         const int tok = i0 + t_local;
         const int m_row = qs + tok;
         bool row_valid = t_local < ntok;
@@ -754,10 +755,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* qsm = sm + kOffQ + qi * kQBytes;
             const float sc = kLog2e * pv.qk_scale;
             const int u = lane & 7;
+            // all rows' lines on their way to L1 first: q (2 lines, lanes 0 and 1 of a row) and the
+            // row of the position table (4 lines, lanes 2..5)
+#pragma unroll 1
+            for (int step = 0; step < 8; ++step) {
+                const int crow = qi * kTileM + 32 * quarter + 4 * step + (lane >> 3), tl_ = crow >> lg, m = qs + i0 + tl_;
+                if (tl_ < ntok && m >= 0 && m < pv.max_position && u < (ALIBI ? 2 : 6)) {
+                    const char* at = u < 2 ? reinterpret_cast<const char*>(P.q + ((size_t)(q0 + i0 + tl_) * Hq + (size_t)h * g +
+                                                                                  crow - tl_ * g) * kD) + 128 * u
+                                           : reinterpret_cast<const char*>(pv.rope + (size_t)m * (kD / 2)) + 128 * (u - 2);
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+                }
+            }
 #pragma unroll 2
             for (int step = 0; step < 8; ++step) {
                 const int tr = 32 * quarter + 4 * step + (lane >> 3), crow = qi * kTileM + tr;
-                const int tl_ = crow / g, m = qs + i0 + tl_;
+                const int tl_ = crow >> lg, m = qs + i0 + tl_;
                 const bool valid = tl_ < ntok && m >= 0 && m < pv.max_position;
                 uint4 w1 = make_uint4(0, 0, 0, 0), w2 = w1;
                 if (valid) {
@@ -996,9 +1009,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-#pragma unroll 4
+#pragma unroll 2
             for (int i = 0; i < 16; ++i) {
-                const int rr = 2 * i + (lane >> 4), crow = qi * kTileM + 32 * quarter + rr, tl_ = crow / g;
+                const int rr = 2 * i + (lane >> 4), crow = qi * kTileM + 32 * quarter + rr, tl_ = crow >> lg;
                 if (tl_ < ntok)
                     reinterpret_cast<uint4*>(P.out + ((size_t)(q0 + i0 + tl_) * Hq + (size_t)h * g + crow - tl_ * g) *
                                                          kD)[lane & 15] =
