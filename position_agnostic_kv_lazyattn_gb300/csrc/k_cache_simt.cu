@@ -15,7 +15,8 @@ namespace lazyattn {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;          // warps of a block
+constexpr int kDecodeWarps = 16;   // of a decode step's, whose few blocks have a whole cache each
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -85,7 +86,7 @@ __device__ __forceinline__ float dot_key(const float* q, int d0, const float (&x
 
 // Block = (query row, query head, request); its warps share the live entries.
 // out NULL: statistics only.
-template <int D>
+template <int D, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32)
     rows_kernel(PoolView pv, Params P, const float* __restrict__ q, float* out) {
     constexpr int J = D / 32;
@@ -278,8 +279,10 @@ int launch_rows(const lazyattn_pool& p, const lazyattn_batch& b, const Params& P
     const int rows = P.decode_qpos ? 1 : b.max_q_len;
     if (rows < 1 || P.total_q < 1) return LAZYATTN_OK;
     const dim3 grid(rows, p.d.n_q_heads, b.num_requests);
-    auto k = p.d.head_dim == 64 ? rows_kernel<64> : rows_kernel<128>;
-    k<<<grid, kWarps * 32, 0, stream>>>(p.view(), P, static_cast<const float*>(q), static_cast<float*>(out));
+    const int warps = P.decode_qpos ? kDecodeWarps : kWarps;
+    auto k = P.decode_qpos ? (p.d.head_dim == 64 ? rows_kernel<64, kDecodeWarps> : rows_kernel<128, kDecodeWarps>)
+                           : (p.d.head_dim == 64 ? rows_kernel<64, kWarps> : rows_kernel<128, kWarps>);
+    k<<<grid, warps * 32, 0, stream>>>(p.view(), P, static_cast<const float*>(q), static_cast<float*>(out));
     return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;
 }
 

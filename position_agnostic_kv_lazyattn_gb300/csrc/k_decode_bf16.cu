@@ -251,7 +251,10 @@ __global__ void __launch_bounds__(kThreads, 3)
         n_w = ce - cb > warp ? (ce - cb - warp + kWarps - 1) / kWarps : 0;
         my_entries = P.entries + (WIN ? (size_t)r * P.list_cap : 0) + cb + warp;
     };
-    if (!WIN) share(P.entry_offsets[r], P.entry_offsets[r + 1]);   // not written by the append
+    if (!WIN) {   // the offsets are not written by the append
+        const int e0 = P.entry_offsets[r], e1 = P.entry_offsets[r + 1];
+        share(e0, MASS ? min(e1, e0 + P.list_cap) : e1);   // the scores have list_cap places a request
+    }
     const uint32_t ring = smem_u32(sm + warp * kStages * kStageBytes);
     volatile int* abort_flag = &s_abort;
 
@@ -721,22 +724,49 @@ __global__ void __launch_bounds__(kThreads, 3)
 
 // Behind a MASS launch. Block = (32 entries, KV head, request): the splits' statistics of
 // the group's heads (one warp a head, one lane a split) give each head's largest score
-// and 1 / sum; the first block also merges the outputs; then thread = (entry,
-// slot) turns its g scores into weights. The scores were written just before: they
-// are read once, mostly from L2.
+// and 1 / sum; the first block also merges the outputs; thread = (two entries, a slot)
+// turns its g scores into weights. Bound by memory (the scores and the mass, read once);
+// everything a thread reads is under way before the statistics are waited for. G: the
+// group's size where its scores are one or two vectors, else 0.
 constexpr int kMassThreads = 256;
 constexpr int kMassEntries = 32;
-template <bool LOCAL>
+template <bool LOCAL, int G>
 __global__ void __launch_bounds__(kMassThreads)
     mass_kernel(PoolView pv, DecodeParams P, const float* mass_in, float* mass_out, float decay) {
+    constexpr int kPer = kMassEntries * kPage / kMassThreads;
     __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
     const int r = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = P.g, S = P.splits;
+    const int g = G ? G : P.g, S = P.splits;
     grid_dep_launch_dependents();
+    const int e0 = P.entry_offsets[r], E = min(P.entry_offsets[r + 1] - e0, P.list_cap);
     grid_dep_wait();
-    const int e0 = P.entry_offsets[r], E = P.entry_offsets[r + 1] - e0;
     const int m = P.qpos[r];
     const size_t rh = (size_t)r * pv.hkv + h;
+
+    const int slot = tid & 15;
+    int n[kPer];
+    float old[kPer];
+    float4 sc[kPer][G ? G / 4 : 1];
+    const float* at[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = (int)blockIdx.x * kMassEntries + k * (kMassThreads / kPage) + (tid >> 4);
+        n[k] = -1;
+        old[k] = 0.f;
+        if (i >= E) continue;
+        const uint64_t e = P.entries[e0 + i];
+        n[k] = max(usable_tokens(pv, e), 0);
+        if (LOCAL && n[k] > 0) {
+            const int d = P.entry_delta[e0 + i];
+            if (d < 0 || d > entry_start(e) || (m >= 0 && (m - d < 0 || m - d >= pv.max_position))) n[k] = 0;
+        }
+        at[k] = P.scores + (((size_t)r * P.list_cap + i) * pv.hkv + h) * (kPage * g) + slot * g;
+        if (G && m >= 0)   // (an unread place of a slot without a token may hold anything: not used)
+#pragma unroll
+            for (int q = 0; q < G / 4; ++q) sc[k][q] = reinterpret_cast<const float4*>(at[k])[q];
+        if (mass_in) old[k] = mass_in[((size_t)(e0 + i) * pv.hkv + h) * kPage + slot];
+    }
+
     if (m >= 0 && warp < g) {
         const float2 x = lane < S ? P.ml[(rh * S + lane) * g + warp] : make_float2(-INFINITY, 0.f);
         float M = x.x;
@@ -766,37 +796,26 @@ __global__ void __launch_bounds__(kMassThreads)
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kMassEntries; k += kMassThreads / kPage) {
-        const int i = (int)blockIdx.x * kMassEntries + k + (tid >> 4), slot = tid & 15;
-        if (i >= E) break;
-        const uint64_t e = P.entries[e0 + i];
-        int n = usable_tokens(pv, e);
-        if (LOCAL && n > 0) {
-            const int d = P.entry_delta[e0 + i];
-            if (d < 0 || d > entry_start(e) || (m >= 0 && (m - d < 0 || m - d >= pv.max_position))) n = 0;
-        }
-        const size_t at = ((size_t)(e0 + i) * pv.hkv + h) * kPage + slot;
+    for (int k = 0; k < kPer; ++k) {
+        const int i = (int)blockIdx.x * kMassEntries + k * (kMassThreads / kPage) + (tid >> 4);
+        if (n[k] < 0) continue;
         float sum = 0.f;
-        if (slot < n) {
+        if (slot < n[k]) {
             if (m >= 0) {
-                const float* s = P.scores + (((size_t)r * P.list_cap + i) * pv.hkv + h) * (kPage * g) + slot * g;
-                if (g == 8) {
-                    const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
-                    sum = fast_exp2(a.x - s_m[0]) * s_inv[0] + fast_exp2(a.y - s_m[1]) * s_inv[1] +
-                          fast_exp2(a.z - s_m[2]) * s_inv[2] + fast_exp2(a.w - s_m[3]) * s_inv[3] +
-                          fast_exp2(b.x - s_m[4]) * s_inv[4] + fast_exp2(b.y - s_m[5]) * s_inv[5] +
-                          fast_exp2(b.z - s_m[6]) * s_inv[6] + fast_exp2(b.w - s_m[7]) * s_inv[7];
-                } else if (g == 4) {
-                    const float4 a = *reinterpret_cast<const float4*>(s);
-                    sum = fast_exp2(a.x - s_m[0]) * s_inv[0] + fast_exp2(a.y - s_m[1]) * s_inv[1] +
-                          fast_exp2(a.z - s_m[2]) * s_inv[2] + fast_exp2(a.w - s_m[3]) * s_inv[3];
+                if (G) {
+#pragma unroll
+                    for (int q = 0; q < G / 4; ++q)
+                        sum += fast_exp2(sc[k][q].x - s_m[4 * q]) * s_inv[4 * q] +
+                               fast_exp2(sc[k][q].y - s_m[4 * q + 1]) * s_inv[4 * q + 1] +
+                               fast_exp2(sc[k][q].z - s_m[4 * q + 2]) * s_inv[4 * q + 2] +
+                               fast_exp2(sc[k][q].w - s_m[4 * q + 3]) * s_inv[4 * q + 3];
                 } else {
-                    for (int j = 0; j < g; ++j) sum += fast_exp2(s[j] - s_m[j]) * s_inv[j];
+                    for (int j = 0; j < g; ++j) sum += fast_exp2(at[k][j] - s_m[j]) * s_inv[j];
                 }
             }
-            if (mass_in) sum += m >= 0 ? decay * mass_in[at] : mass_in[at];
+            if (mass_in) sum += m >= 0 ? decay * old[k] : old[k];
         }
-        mass_out[at] = sum;
+        mass_out[((size_t)(e0 + i) * pv.hkv + h) * kPage + slot] = sum;
     }
 }
 
@@ -975,7 +994,10 @@ int launch_decode_mass_bf16(const lazyattn_pool& p, const lazyattn_batch& b, con
     rc = launch(p, b, P, P.g <= 4 ? MASS4 : MASS8, stream);
     if (rc != LAZYATTN_OK) return rc;
     const dim3 grid((P.list_cap + kMassEntries - 1) / kMassEntries, p.d.n_kv_heads, b.num_requests);
-    auto kern = p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL ? mass_kernel<true> : mass_kernel<false>;
+    const bool local = p.d.key_storage == LAZYATTN_KEYS_DOC_LOCAL;
+    auto kern = P.g == 8   ? (local ? mass_kernel<true, 8> : mass_kernel<false, 8>)
+                : P.g == 4 ? (local ? mass_kernel<true, 4> : mass_kernel<false, 4>)
+                           : (local ? mass_kernel<true, 0> : mass_kernel<false, 0>);
     if (launch_dependent(kern, grid, dim3(kMassThreads), 0, stream, p.view(), P, mass_in, mass_out, decay) != cudaSuccess)
         return LAZYATTN_ECUDA;
     return cudaGetLastError() == cudaSuccess ? LAZYATTN_OK : LAZYATTN_ECUDA;

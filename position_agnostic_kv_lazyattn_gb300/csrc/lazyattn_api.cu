@@ -464,15 +464,17 @@ int lazyattn_decode_window(lazyattn_pool_t pool, const lazyattn_batch* batch, co
     if (!window_ok(window, sinks) || !q || !k_new || !v_new || !out || !workspace) return LAZYATTN_EINVAL;
     if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) || !aligned256(workspace))
         return LAZYATTN_EINVAL;
-    if (workspace_bytes < lazyattn_window_workspace_size(pool, LAZYATTN_OP_DECODE, batch, window, sinks))
-        return LAZYATTN_EWORKSPACE;
+    const bool bf16 = pool->d.dtype == LAZYATTN_BF16;
+    DecodeWs layout = {};
+    if (bf16) layout = decode_window_ws_layout(*pool, *batch, window, sinks);
+    if (workspace_bytes < (bf16 ? layout.total : qpos_bytes(batch))) return LAZYATTN_EWORKSPACE;
     rc = check_device(pool);
     if (rc != LAZYATTN_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (pool->d.dtype == LAZYATTN_BF16)
+    if (bf16)
         return launch_decode_window_bf16(*pool, *batch, static_cast<const __nv_bfloat16*>(q), k_new, v_new,
-                                         static_cast<__nv_bfloat16*>(out), window, sinks, workspace,
-                                         decode_window_ws_layout(*pool, *batch, window, sinks), st);
+                                         static_cast<__nv_bfloat16*>(out), window, sinks, workspace, layout,
+                                         st);
     int32_t* qpos = static_cast<int32_t*>(workspace);
     rc = launch_decode_append(*pool, *batch, k_new, v_new, qpos, st);
     if (rc != LAZYATTN_OK) return rc;
@@ -507,14 +509,17 @@ int lazyattn_decode_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, cons
     if (!q || !k_new || !v_new || !out || !workspace || !mass_ok(mass_in, mass_out, decay)) return LAZYATTN_EINVAL;
     if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(out) || !aligned256(workspace))
         return LAZYATTN_EINVAL;
-    if (workspace_bytes < lazyattn_workspace_size(pool, LAZYATTN_OP_DECODE_MASS, batch)) return LAZYATTN_EWORKSPACE;
+    const bool bf16 = pool->d.dtype == LAZYATTN_BF16;
+    DecodeWs layout = {};
+    if (bf16) layout = decode_mass_ws_layout(*pool, *batch);
+    if (workspace_bytes < (bf16 ? layout.total : lazyattn_workspace_size(pool, LAZYATTN_OP_DECODE_MASS, batch)))
+        return LAZYATTN_EWORKSPACE;
     rc = check_device(pool);
     if (rc != LAZYATTN_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (pool->d.dtype == LAZYATTN_BF16)
+    if (bf16)
         return launch_decode_mass_bf16(*pool, *batch, static_cast<const __nv_bfloat16*>(q), k_new, v_new,
-                                       static_cast<__nv_bfloat16*>(out), mass_in, mass_out, decay, workspace,
-                                       decode_mass_ws_layout(*pool, *batch), st);
+                                       static_cast<__nv_bfloat16*>(out), mass_in, mass_out, decay, workspace, layout, st);
     int32_t* qpos = static_cast<int32_t*>(workspace);
     rc = launch_decode_append(*pool, *batch, k_new, v_new, qpos, st);
     if (rc != LAZYATTN_OK) return rc;

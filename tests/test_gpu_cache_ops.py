@@ -452,6 +452,66 @@ def test_evict_refuses_bad_tables_on_the_device(L):
         assert set(touched) <= set(pages[offs[1]:offs[2]])
 
 
+# ------------------------------------------------------------------------------------------------ long tables
+
+def with_empty_entries(L, s, lead, every):
+    """The scenario's table with `lead` empty entries in front of each request's and `every` behind each of its entries."""
+    b, out, offs = s.batch, [], [0]
+    empty = L.pack_entries([0], [0], [0], [0])[0]
+    for r in range(len(s.rows)):
+        words = [empty] * lead
+        for e in b.entries_host[b.offsets_host[r]:b.offsets_host[r + 1]]:
+            words.append(e)
+            if not oracle.unpack_entry(int(e))[3]:          # the writable run stays in one piece
+                words += [empty] * every
+        out += words
+        offs.append(len(out))
+    b2 = b.with_entries(np.array(out, np.uint64), b.flags)
+    b2.offsets_host = np.array(offs, np.int32)
+    b2.entry_offsets = torch.from_numpy(b2.offsets_host).cuda()
+    b2.max_entries = int(np.max(np.diff(b2.offsets_host)))
+    b2.c = L.lazyattn.make_batch(b2.num_requests, b2.max_entries, b2.entries, b2.entry_offsets, b.q_offsets, b.q_start,
+                                 b.max_q_len, b.total_q, b.flags)
+    s.batch = b2
+
+
+@pytest.mark.parametrize("lead,every", [(70000, 0), (0, 900), (3, 2)])
+def test_tables_of_many_entries(L, lead, every):
+    """Tables past the prefill's 8192 marked tiles and past what an evicting block holds at a time, most entries empty."""
+    s = Scenario(L, [([700, 33, 500], 40, 40), ([5, 100], 17, 9)], seed=34, extra=200)
+    with_empty_entries(L, s, lead, every)
+    check_prefill_window(L, s, 300, 3)
+    check_prefill_mass(L, s, 1.0, False)
+    check_evict(L, s, weights_of(s, "ties", np.random.default_rng(35)), 333, 4, 50)
+    check_evict(L, s, weights_of(s, "equal", np.random.default_rng(36)), 1000, 0, 0)
+    check_decode_window(L, s, 300, 3, 1)
+    s = Scenario(L, [([700, 33, 500], 40, 0), ([5, 100], 17, 0)], seed=37)
+    with_empty_entries(L, s, lead, every)
+    check_decode_mass(L, s, 1.0, 2)
+
+
+def test_calls_on_a_stream_of_their_own(L):
+    """stream= given: the calls run there, behind work that fills their inputs, with another stream current."""
+    s = Scenario(L, [([300, 150], 64, 64)], seed=38, extra=40)
+    side = torch.cuda.Stream()
+    q, want = s.dev(s.q), s.empty(64, s.hq, s.d)
+    wsp, wsm = workspace(L, s, L.LAZYATTN_OP_PREFILL, 100, 4), workspace(L, s, L.LAZYATTN_OP_PREFILL_MASS)
+    L.lazyattn_prefill_window(s.pool.handle, s.batch.c, q, want, 100, 4, *wsp)
+    mass = torch.empty(s.n_entries(), s.hkv, 16, device="cuda")
+    L.lazyattn_prefill_mass(s.pool.handle, s.batch.c, q, None, mass, 1.0, *wsm)
+    batch, kept, _ = s.batch.evict(s.pool, mass, 50, 2, 8)
+    torch.cuda.synchronize()
+    late, out, mass2 = torch.zeros_like(q), torch.zeros_like(want), torch.empty_like(mass)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(q)
+    L.lazyattn_prefill_window(s.pool.handle, s.batch.c, late, out, 100, 4, *wsp, stream=side)
+    L.lazyattn_prefill_mass(s.pool.handle, s.batch.c, late, None, mass2, 1.0, *wsm, stream=side)
+    batch2, kept2, _ = s.batch.evict(s.pool, mass2, 50, 2, 8, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(mass, mass2) and torch.equal(kept, kept2)
+
+
 # ------------------------------------------------------------------------------------------------ refusals
 
 def test_refusals(L):
