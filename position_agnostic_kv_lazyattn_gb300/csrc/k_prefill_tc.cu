@@ -746,12 +746,72 @@ __global__ void __launch_bounds__(kThreads, 1)
             row_valid = false;
         }
 
-        // Q: rotated at the row's position, scaled by log2(e) times the pool's logit scale
-        // (1/sqrt(D)), fp16, 128B-swizzled K-major. Eight lanes take a row (lane u: dims 8u.. of both
-        // halves), four rows at a time: a load then touches four lines, not a line per lane. (A
-        // thread per row kept the load units busy for most of 7 us, and the producer's first
-        // block-table read waited behind them.)
-        {
+        // Q row: rotate at m_row, scale by log2(e) times the pool's logit scale (1/sqrt(D)),
+        // fp16, 128B-swizzled K-major
+        if (!WIN) {
+            uint8_t* qsm = sm + kOffQ + qi * kQBytes;
+            const float sc = kLog2e * pv.qk_scale;
+            const __nv_bfloat16* qp_ = P.q + ((size_t)(q0 + tok) * Hq + (size_t)h * g + jh) * kD;
+            const float* cs = reinterpret_cast<const float*>(pv.rope + (size_t)(row_valid ? m_row : 0) * (kD / 2));
+            // The row's position-table line (512 B) is fetched into L1 while the
+            // q words load; each half of the row's dims loads its q words together.
+            if (!ALIBI && row_valid) {
+#pragma unroll
+                for (int l = 0; l < 4; ++l) asm volatile("prefetch.global.L1 [%0];" ::"l"(cs + 32 * l));
+            }
+#pragma unroll 1
+            for (int h4 = 0; h4 < 2; ++h4) {
+                uint4 qa[4], qb[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int u = 4 * h4 + i;
+                    qa[i] = row_valid ? __ldg(reinterpret_cast<const uint4*>(qp_ + (INTER ? 16 * u : 8 * u)))
+                                      : make_uint4(0, 0, 0, 0);
+                    qb[i] = row_valid ? __ldg(reinterpret_cast<const uint4*>(qp_ + (INTER ? 16 * u + 8 : 64 + 8 * u)))
+                                      : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int u = 4 * h4 + i;
+                    uint4 w1 = make_uint4(0, 0, 0, 0), w2 = w1;
+                    if (row_valid) {
+                        float x1[8], x2[8];
+                        uint4 a = qa[i], b = qb[i];
+                        if (INTER) deinterleave16(a, b, a, b);
+                        unpack8(a, x1);
+                        unpack8(b, x2);
+                        float n2 = 0.f;   // input range: rotated, scaled pairs must stay finite in fp16
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) n2 = fmaxf(n2, fmaf(x1[v], x1[v], x2[v] * x2[v]));
+                        if (!(n2 * sc * sc <= kMaxPairNorm2)) record_error(pv.status, LAZYATTN_ERANGE);
+                        const float4* c4 = reinterpret_cast<const float4*>(cs + 16 * u);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const float4 f = ALIBI ? make_float4(1.f, 0.f, 1.f, 0.f) : __ldg(c4 + v);
+                            const float a0 = x1[2 * v], z0 = x2[2 * v], a1 = x1[2 * v + 1], z1 = x2[2 * v + 1];
+                            x1[2 * v] = (a0 * f.x - z0 * f.y) * sc;
+                            x2[2 * v] = (a0 * f.y + z0 * f.x) * sc;
+                            x1[2 * v + 1] = (a1 * f.z - z1 * f.w) * sc;
+                            x2[2 * v + 1] = (a1 * f.w + z1 * f.z) * sc;
+                        }
+                        w1 = pack8_h(x1);
+                        w2 = pack8_h(x2);
+                    }
+                    *reinterpret_cast<uint4*>(qsm + sw128_offset(trow, u)) = w1;
+                    *reinterpret_cast<uint4*>(qsm + kQChunk + sw128_offset(trow, u)) = w2;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_qready));
+        }
+        // Under a window, where a CTA has few tiles and starts count: eight lanes take a row
+        // (lane u: dims 8u.. of both halves), four rows at a time, so that a load touches four lines, not a
+        // line per lane. (A thread per row keeps the load units busy for most of 7 us, and the producer's
+        // first block-table read waits behind them: an 8192-token prompt under a window of 1024
+        // takes 266 us that way and 244 this way, output rows included; without a window, where tiles
+        // count, it is the other way round: 1.340 ms against 1.369 for 32 prompts of 20 documents.)
+        if (WIN) {
             uint8_t* qsm = sm + kOffQ + qi * kQBytes;
             const float sc = kLog2e * pv.qk_scale;
             const int u = lane & 7;
@@ -820,8 +880,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const TileInfo& info = s_info[is];
             if (info.j < 0) break;
-            // a warp whose rows all see every key of the tile skips the masking
-            const bool wfull = __all_sync(0xffffffffu, row_valid && m_row >= info.full_from && (!WIN || m_row < info.full_to));
+            // a warp whose rows all see every key of the tile skips the masking (under a window
+            // rows without a query count as such: their sums are dropped at the end)
+            const bool wfull = __all_sync(0xffffffffu, (row_valid && m_row >= info.full_from && (!WIN || m_row < info.full_to)) ||
+                                                           (WIN && !row_valid && info.full_from != INT_MAX));
             // visibility of the tile's keys to this row: bit i of visN is key
             // 32N + i (pages 2N and 2N+1 hold slots [0, lim) of their 16)
             uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
@@ -960,6 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&bar_pfull[qi]));
         }
 
+        if (WIN && !row_valid) l_run = 0.f;
         // epilogue: O / l -> bf16 rows of out; or, when the request's tiles are
         // split over several CTAs, this CTA's unnormalised O with its reference
         // maximum and sum (merged by prefill_combine_kernel)
@@ -986,36 +1049,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (active) {
             if (ok && k >= 1) ok = mbar_wait(smem_u32(&bar_odone[qi]), (k - 1) & 1, abort_flag);
             tc_fence_after();
-            // Rows go through this warp's 8 KB of its Q tile (whose last QK is done), 16-byte units
-            // XORed with the row, so that the stores to memory are whole rows: two a store, not a
-            // line per lane.
             const float inv = (ok && l_run > 0.f) ? 1.f / l_run : 0.f;
-            uint8_t* stage = sm + kOffQ + qi * kQBytes + quarter * 32 * 256;
+            if (!WIN) {
+                __nv_bfloat16* op = P.out + ((size_t)(q0 + tok) * Hq + (size_t)h * g + jh) * kD;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                if (k >= 1 && ok) {
-                    tmem_ld32(to + 32 * c, v);
-                } else {
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    if (k >= 1 && ok) {
+                        tmem_ld32(to + 32 * c, v);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0u;
-                }
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    }
+                    if (t_local < ntok) {
+                        uint4* dst = reinterpret_cast<uint4*>(op + 32 * c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float* f = reinterpret_cast<const float*>(v + 8 * i);
-                    *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * c + i) ^ (lane & 7)) << 4)) =
-                        make_uint4(pack_bf2(f[0] * inv, f[1] * inv), pack_bf2(f[2] * inv, f[3] * inv),
-                                   pack_bf2(f[4] * inv, f[5] * inv), pack_bf2(f[6] * inv, f[7] * inv));
+                        for (int i = 0; i < 4; ++i) {
+                            const float* f = reinterpret_cast<const float*>(v + 8 * i);
+                            dst[i] = make_uint4(pack_bf2(f[0] * inv, f[1] * inv), pack_bf2(f[2] * inv, f[3] * inv),
+                                                pack_bf2(f[4] * inv, f[5] * inv), pack_bf2(f[6] * inv, f[7] * inv));
+                        }
+                    }
                 }
-            }
-            __syncwarp();
+            } else {
+                // Rows go through this warp's 8 KB of its Q tile (whose last QK is done), 16-byte units
+                // XORed with the row, so that the stores to memory are whole rows: two a store, not a
+                // line per lane.
+                uint8_t* stage = sm + kOffQ + qi * kQBytes + quarter * 32 * 256;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    if (k >= 1 && ok) {
+                        tmem_ld32(to + 32 * c, v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float* f = reinterpret_cast<const float*>(v + 8 * i);
+                        *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * c + i) ^ (lane & 7)) << 4)) =
+                            make_uint4(pack_bf2(f[0] * inv, f[1] * inv), pack_bf2(f[2] * inv, f[3] * inv),
+                                       pack_bf2(f[4] * inv, f[5] * inv), pack_bf2(f[6] * inv, f[7] * inv));
+                    }
+                }
+                __syncwarp();
 #pragma unroll 2
-            for (int i = 0; i < 16; ++i) {
-                const int rr = 2 * i + (lane >> 4), crow = qi * kTileM + 32 * quarter + rr, tl_ = crow >> lg;
-                if (tl_ < ntok)
-                    reinterpret_cast<uint4*>(P.out + ((size_t)(q0 + i0 + tl_) * Hq + (size_t)h * g + crow - tl_ * g) *
-                                                         kD)[lane & 15] =
-                        *reinterpret_cast<const uint4*>(stage + rr * 256 + (((lane & 15) ^ (rr & 7)) << 4));
+                for (int i = 0; i < 16; ++i) {
+                    const int rr = 2 * i + (lane >> 4), crow = qi * kTileM + 32 * quarter + rr, tl_ = crow >> lg;
+                    if (tl_ < ntok)
+                        reinterpret_cast<uint4*>(P.out + ((size_t)(q0 + i0 + tl_) * Hq + (size_t)h * g + crow - tl_ * g) *
+                                                             kD)[lane & 15] =
+                            *reinterpret_cast<const uint4*>(stage + rr * 256 + (((lane & 15) ^ (rr & 7)) << 4));
+                }
             }
         }
     }
