@@ -609,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (PASS == 1) {
                 if (j < 0) break;
-                const bool wfull = __all_sync(0xffffffffu, row_valid && m_row >= info.full_from);
+                // (rows without a query count as seeing all: their sums are dropped at the end)
+                const bool wfull = __all_sync(0xffffffffu, row_valid ? m_row >= info.full_from : info.full_from != INT_MAX);
                 ok = mbar_wait(smem_u32(&bar_sfull[wg]), use & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
