@@ -472,7 +472,8 @@ int lazyattn_decode_noalloc(lazyattn_pool_t pool, const lazyattn_batch* batch, c
 size_t lazyattn_window_workspace_size(lazyattn_pool_t pool, int32_t op, const lazyattn_batch* batch,
                                       int32_t window, int32_t sinks);
 
-/* lazyattn_prefill under a window. workspace is optional, as there. */
+/* lazyattn_prefill under a window (bf16 pools: Hq / Hkv of 1, 2, 4 or 8, as there;
+ * else EINVAL). workspace is optional, as there. */
 int lazyattn_prefill_window(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, void* out,
                             int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes, void* stream);
 
@@ -501,7 +502,8 @@ int lazyattn_decode_window(lazyattn_pool_t pool, const lazyattn_batch* batch, co
  * q_offsets, q_start, keys visible up to a row's own position) observe the cache;
  * no output is computed. Typically the last rows of a prompt, before the cache is cut down.
  * Rows that see no key, and requests without rows, add nothing. Workspace:
- * lazyattn_workspace_size(LAZYATTN_OP_PREFILL_MASS), required, no zero-fill needed. */
+ * lazyattn_workspace_size(LAZYATTN_OP_PREFILL_MASS), required; no zero-fill needed, and
+ * left in any state (zero it again before a call that wants zeros gets it). */
 int lazyattn_prefill_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const float* mass_in,
                           float* mass_out, float decay, void* workspace, size_t workspace_bytes, void* stream);
 
