@@ -153,13 +153,14 @@ __device__ int find_append_entry(const uint64_t* entries, int e0, int e1, int la
 }
 
 // Append k_new/v_new of request r into its tail page (called by a whole block).
+// Returns the entry's new value, and its index in `at` (-1: nothing appended), to every thread.
 // MODE: 0 stores k as given (position-free keys); 1 rotates it at its logical
 // position (pre-rotated pages of the materialising baseline); 2 at its
 // document-local position, logical - entry_delta (doc-local pools).
 template <typename T, int MODE>
-__device__ __forceinline__ void append_token(const PoolView& pv, uint64_t* entries, const int32_t* entry_offsets,
+__device__ __forceinline__ uint64_t append_token(const PoolView& pv, uint64_t* entries, const int32_t* entry_offsets,
                                              const T* __restrict__ k_new, const T* __restrict__ v_new, int32_t* qpos,
-                                             const int32_t* entry_delta, int r) {
+                                             const int32_t* entry_delta, int r, int& at) {
     constexpr bool PREROT = MODE != 0;
     __shared__ int s_entry;
     __shared__ uint64_t s_e;
@@ -183,7 +184,8 @@ __device__ __forceinline__ void append_token(const PoolView& pv, uint64_t* entri
         }
     }
     __syncthreads();
-    if (s_entry < 0) return;
+    at = s_entry;
+    if (at < 0) return 0ull;
     const uint64_t e = s_e;
     const uint32_t page = entry_page(e);
     const int slot = entry_nvalid(e);
@@ -192,7 +194,7 @@ __device__ __forceinline__ void append_token(const PoolView& pv, uint64_t* entri
         const int delta = entry_delta[s_entry];
         if (delta < 0 || delta > entry_start(e)) {
             if (threadIdx.x == 0) record_error(pv.status, LAZYATTN_ERANGE);
-            return;
+            return e;
         }
         pos -= delta;
     }
@@ -272,10 +274,12 @@ __device__ __forceinline__ void append_token(const PoolView& pv, uint64_t* entri
         vp[dst + d + half] = v_new[src + d + half];
     }
     __syncthreads();
+    const uint64_t now = make_entry(page, entry_start(e), slot + 1, true);
     if (threadIdx.x == 0) {
         __threadfence();
-        entries[s_entry] = make_entry(page, entry_start(e), slot + 1, true);
+        entries[at] = now;
     }
+    return now;
 }
 
 // One block per request, launched as a programmatic dependent of the previous
@@ -287,7 +291,8 @@ __global__ void decode_append_kernel(PoolView pv, uint64_t* entries, const int32
                                      const int32_t* entry_delta) {
     grid_dep_launch_dependents();
     grid_dep_wait();
-    append_token<T, MODE>(pv, entries, entry_offsets, k_new, v_new, qpos, entry_delta, blockIdx.x);
+    int at;
+    append_token<T, MODE>(pv, entries, entry_offsets, k_new, v_new, qpos, entry_delta, blockIdx.x, at);
 }
 
 // The append of a windowed step, then the request's live list: the entries with a
@@ -305,19 +310,28 @@ __global__ void __launch_bounds__(kListThreads)
     const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dep_launch_dependents();
     grid_dep_wait();
-    append_token<__nv_bfloat16, MODE>(pv, entries, entry_offsets, k_new, v_new, qpos, entry_delta, r);
-    __syncthreads();   // the table entry and qpos written by thread 0
-    const int m = qpos[r];
+    // the first round's entries are read before the append, which changes one of them
     const int e0 = entry_offsets[r], e1 = entry_offsets[r + 1];
-    int done = 0;
-    for (int base = e0; base < e1 && m >= 0; base += kListThreads * kListRun) {
-        uint64_t e[kListRun];
-        uint32_t live = 0;
+    uint64_t e[kListRun];
+    auto load = [&](int base) {
 #pragma unroll
         for (int j = 0; j < kListRun; ++j) {
             const int i = base + threadIdx.x * kListRun + j;
             e[j] = i < e1 ? entries[i] : 0ull;
         }
+    };
+    load(e0);
+    int appended;
+    const uint64_t tail = append_token<__nv_bfloat16, MODE>(pv, entries, entry_offsets, k_new, v_new, qpos, entry_delta, r,
+                                                            appended);
+    const int m = appended < 0 ? -1 : entry_start(tail) + entry_nvalid(tail) - 1;
+    int done = 0;
+    for (int base = e0; base < e1 && m >= 0; base += kListThreads * kListRun) {
+        if (base > e0) load(base);
+        uint32_t live = 0;
+#pragma unroll
+        for (int j = 0; j < kListRun; ++j)
+            if (base + threadIdx.x * kListRun + j == appended) e[j] = tail;
 #pragma unroll
         for (int j = 0; j < kListRun; ++j) {
             const int n = entry_nvalid(e[j]), a = entry_start(e[j]), b = min(a + n - 1, m);
