@@ -149,7 +149,10 @@ def _check(rc: int, where: str):
 def _ptr(t) -> Optional[int]:
     if t is None:
         return None
-    return t.data_ptr() if hasattr(t, "data_ptr") else int(t)
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        return int(t)
 
 
 def _stream(stream) -> Optional[int]:
