@@ -1,9 +1,9 @@
 // Attention mass of a batch's query rows (bf16 pools) on tcgen05 / TMEM:
 //     mass[n] = sum over rows i of 2^(s_in - M_i) / L_i,   L_i = sum over n of 2^(s_in - M_i)
 // with s the scores in the log2 domain. L_i is not known before all of row i's
-// scores are, and keeping the scores (4 bytes each, against 0.75 ns of tensor time for 256
-// of them) would take more memory time than forming them again, so there are two passes over the
-// keys and a reduction:
+// scores are, and keeping the scores takes more memory time than forming them again (a 128 x 128
+// tile of them is 64 KB to write and to read, 2.9 us of an SM's share of the bandwidth; its MMAs
+// take 0.8 us), so there are two passes over the keys and a reduction:
 //   pass 1  running maximum and sum of each row (thread = row)
 //   pass 2  the rows' weights, summed per key: one float per key and block of 128
 //           rows goes to the workspace
@@ -30,7 +30,7 @@
 // the same 8 columns; it adds those, 7 shuffles join the 8 threads of a column, and the
 // four warps meet in shared memory. Every wait is bounded, as in the prefill kernel.
 //
-// Measured (GB300): 8 requests of ~17,500 keys, 33..128 rows, 32/8 heads: 705 us, of which
+// Measured (GB300): 8 requests of ~17,400 keys, 100..128 rows, 32/8 heads: 705 us, of which
 // the MMAs are 430 (67 cycles each) and the rest the issuer's gaps between tiles (~500
 // cycles) and the roles' contention: without the threads' arithmetic on the scores a pass takes
 // 298 us of its 343, without the rotation 291. 16 requests of 2,112 keys, 64 rows: 103 us,

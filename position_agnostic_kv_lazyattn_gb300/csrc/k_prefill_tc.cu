@@ -884,9 +884,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const TileInfo& info = s_info[is];
             if (info.j < 0) break;
             // a warp whose rows all see every key of the tile skips the masking (under a window
-            // rows without a query count as such: their sums are dropped at the end)
+            // rows past the CTA's last count as such: nothing of theirs is stored)
             const bool wfull = __all_sync(0xffffffffu, (row_valid && m_row >= info.full_from && (!WIN || m_row < info.full_to)) ||
-                                                           (WIN && !row_valid && info.full_from != INT_MAX));
+                                                           (WIN && t_local >= ntok && info.full_from != INT_MAX));
             // visibility of the tile's keys to this row: bit i of visN is key
             // 32N + i (pages 2N and 2N+1 hold slots [0, lim) of their 16)
             uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
@@ -1025,7 +1025,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&bar_pfull[qi]));
         }
 
-        if (WIN && !row_valid) l_run = 0.f;
         // epilogue: O / l -> bf16 rows of out; or, when the request's tiles are
         // split over several CTAs, this CTA's unnormalised O with its reference
         // maximum and sum (merged by prefill_combine_kernel)

@@ -103,6 +103,35 @@ def test_prefill_window_rows_that_see_nothing(L):
     check_out(got, want, "bf16")
 
 
+@pytest.mark.parametrize("mode", ["rope", "alibi"])
+@pytest.mark.parametrize("start", [-3, 485])
+def test_rows_out_of_range(L, mode, start):
+    """Rows before position 0 or past the position table: zeros, no weight, reported; the others as ever."""
+    s = Scenario(L, [([300, 100], 40, 8)], mode, seed=39, spare=2)
+    top = s.pool.max_position                          # 440 + 32 + 16
+    n = 8
+    q = s.normal(n, s.hq, s.d) * 2
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    qs = torch.tensor([start], dtype=torch.int32, device="cuda")
+    c = L.lazyattn.make_batch(1, s.batch.max_entries, s.batch.entries, s.batch.entry_offsets, off, qs, n, n)
+    inside = [i for i in range(n) if 0 <= start + i < top]
+    assert 0 < len(inside) < n
+    out = s.empty(n, s.hq, s.d)
+    L.lazyattn_prefill_window(s.pool.handle, c, s.dev(q), out, 90, 2)
+    assert s.pool.device_status() == L.LAZYATTN_ERANGE
+    got = out.float().cpu().numpy()
+    ref = attend(s.spec, q[inside], s.k[0], s.v[0], start + np.array(inside), s.pos[0], 90, 2)
+    check_out(got[inside], ref, "bf16")
+    assert np.all(np.delete(got, inside, 0) == 0)
+    size = L.lazyattn_workspace_size(s.pool.handle, L.LAZYATTN_OP_PREFILL_MASS, c)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    mass = torch.empty(s.n_entries(), s.hkv, 16, device="cuda")
+    L.lazyattn_prefill_mass(s.pool.handle, c, s.dev(q), None, mass, 1.0, ws, size)
+    assert s.pool.device_status() == L.LAZYATTN_ERANGE
+    ref = attend(s.spec, q[inside], s.k[0], s.v[0], start + np.array(inside), s.pos[0])
+    check_mass(mass.cpu().numpy(), s.mass_of([ref.mass]), ref.reach)
+
+
 def decode_state(s):
     return [k.copy() for k in s.k], [v.copy() for v in s.v], [p.copy() for p in s.pos]
 
