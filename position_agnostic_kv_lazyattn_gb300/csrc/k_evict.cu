@@ -20,6 +20,7 @@
 // selection 26 (latency of its phases) and the copy 86 (537 MB at 6.2 TB/s: bound by memory); one request
 // of 2,118 tokens cut to 512: 14 us.
 #include <cooperative_groups.h>
+#include <limits.h>
 
 #include "internal.h"
 
@@ -69,6 +70,29 @@ __device__ __forceinline__ int block_scan(int v, int (&warp_sum)[kWarps], int& t
     return before + x - v;
 }
 
+// Largest value of the threads before this one (0 for the first; values are 0 or more), and of all.
+__device__ __forceinline__ int block_max_before(int v, int (&warp_max)[kWarps], int& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x = max(x, a);
+    }
+    __syncthreads();   // the values of an earlier call have been read
+    if (lane == 31) warp_max[warp] = x;
+    __syncthreads();
+    int before = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before = max(before, warp_max[w]);
+        all = max(all, warp_max[w]);
+    }
+    const int up = __shfl_up_sync(0xffffffffu, x, 1);
+    return lane ? max(before, up) : before;
+}
+
 struct EvictParams {
     const uint64_t* entries;
     const int32_t* entry_offsets;
@@ -85,6 +109,7 @@ struct Shared {
     int hist[kDigits][kBins];
     int scan[kWarps];
     int tokens, bad;           // of this block's share
+    int first, end;            // its first token's position (INT_MAX: none), the largest position + 1 of its tokens
     int sure, equal;           // tokens kept for certain, tokens equal to the threshold
     int digit, want;
     int warp_sure[kWarps], warp_equal[kWarps];
@@ -107,30 +132,43 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(PoolView pv, EvictPa
     int* first = reinterpret_cast<int*>(dyn + (size_t)P.seg * kPage);   // [seg]: tokens before the entry, in the share
 
     for (int b = tid; b < kDigits * kBins; b += kThreads) (&S.hist[0][0])[b] = 0;
-    if (tid == 0) S.bad = 0;
+    if (tid == 0) {
+        S.bad = 0;
+        S.first = INT_MAX;
+        S.end = 0;
+    }
     __syncthreads();
 
     // Count the share's tokens and check the table: pages and positions in range, entries
-    // with tokens ascending in position (each against the last one before it that has tokens).
+    // with tokens ascending in position (each starts at or past the ends of all before it).
     // Leaves the segment's `first`, and the tokens before the segment in `before`.
     auto load_entries = [&](int seg, int before, bool check) {
         const int b0 = a0 + seg * P.seg, n_here = min(P.seg, a1 - b0);
-        int n[kRun], sum = 0;
+        int n[kRun], sum = 0, begin[kRun], end = 0;
 #pragma unroll
         for (int j = 0; j < kRun; ++j) {
             const int i = tid * kRun + j;
             const uint64_t e = i < n_here ? P.entries[e0 + b0 + i] : 0ull;
             n[j] = min(entry_nvalid(e), kPage);
             sum += n[j];
+            begin[j] = entry_start(e);
             if (check && n[j] > 0) {
                 if (!entry_ok(pv, e)) S.bad = 1;
-                for (int k = b0 + i - 1; k >= 0; --k) {
-                    const uint64_t f = P.entries[e0 + k];
-                    if (entry_nvalid(f) == 0) continue;
-                    if (entry_start(f) + entry_nvalid(f) > entry_start(e)) S.bad = 1;
-                    break;
-                }
+                end = max(end, begin[j] + n[j]);
             }
+        }
+        if (check) {
+            int all;
+            int so_far = max(block_max_before(end, S.scan, all), S.end);   // S.end: of the segments before
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) {
+                if (n[j] == 0) continue;
+                if (begin[j] < so_far) S.bad = 1;
+                so_far = max(so_far, begin[j] + n[j]);
+                atomicMin(&S.first, begin[j]);
+            }
+            __syncthreads();   // S.end has been read
+            if (tid == 0) S.end = max(S.end, all);
         }
         int total;
         int at = before + block_scan(sum, S.scan, total);
@@ -149,10 +187,12 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(PoolView pv, EvictPa
         if (tid == 0) S.tokens = tokens;
     }
     cluster.sync();
-    int n_tok = 0, base = 0;
+    int n_tok = 0, base = 0, end = 0;
     bool bad = false;
     for (int c = 0; c < C; ++c) {
         const Shared* o = cluster.map_shared_rank(&S, c);
+        bad = bad || o->first < end;
+        end = max(end, o->end);
         if (c < rank) base += o->tokens;
         n_tok += o->tokens;
         bad = bad || o->bad != 0;

@@ -519,6 +519,31 @@ def test_tables_of_many_entries(L, lead, every):
     check_decode_mass(L, s, 1.0, 2)
 
 
+@pytest.mark.parametrize("a,b", [(0, 1), (3, 700), (700, 701), (1, 60000), (59000, 60000)])
+def test_evict_finds_disorder_anywhere(L, a, b):
+    """Two tokens' entries exchanged in a table that several blocks and segments share."""
+    s = Scenario(L, [([], 16 * 60, 0), ([40], 5, 0)], seed=40, extra=12)
+    with_empty_entries(L, s, 0, 0)
+    words = list(s.batch.entries_host)
+    empty = L.pack_entries([0], [0], [0], [0])[0]
+    table = np.full(61000, empty, np.uint64)
+    at = np.unique(np.r_[[0, 1, 3, 700, 701, 59000, 60000], np.linspace(5, 58000, 53).astype(int)])[:60]
+    table[at] = words[:len(at)]
+    fine = table.copy()
+    table[[a, b]] = table[[b, a]]
+    for ent, bad in [(fine, False), (table, True)]:
+        e = torch.from_numpy(ent.view(np.int64).copy()).cuda()
+        off = torch.tensor([0, len(ent)], dtype=torch.int32, device="cuda")
+        c = L.lazyattn.make_batch(1, len(ent), e, off)
+        dst = torch.from_numpy(L.pack_entries(s.pool.alloc_pages(4), [0] * 4, [0] * 4, [1] * 4).view(np.int64).copy()).cuda()
+        d_off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+        kept = torch.zeros(1, s.hkv, 50, dtype=torch.int32, device="cuda")
+        mass = torch.rand(len(ent), s.hkv, 16, device="cuda")
+        L.lazyattn_evict(s.pool.handle, c, mass, 50, 4, 8, dst, d_off, kept)
+        assert (s.pool.device_status() == L.LAZYATTN_ERANGE) == bad
+        assert bool((kept == -1).all()) == bad and bool((kept >= 0).all()) != bad
+
+
 def test_calls_on_a_stream_of_their_own(L):
     """stream= given: the calls run there, behind work that fills their inputs, with another stream current."""
     s = Scenario(L, [([300, 150], 64, 64)], seed=38, extra=40)
