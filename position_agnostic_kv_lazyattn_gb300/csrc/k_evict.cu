@@ -119,6 +119,9 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(PoolView pv, EvictPa
     extern __shared__ __align__(16) uint32_t dyn[];
     __shared__ Shared S;
     cg::cluster_group cluster = cg::this_cluster();
+    // The copy's blocks wait for this grid's end before they read anything it writes: 13.7 us for 14.0 a small
+    // call in a graph, 115 for 116 with 32 requests.
+    grid_dep_launch_dependents();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int h = blockIdx.y, r = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hkv = pv.hkv;

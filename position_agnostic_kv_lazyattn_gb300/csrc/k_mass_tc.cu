@@ -188,6 +188,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int s_abort;
     __shared__ float2 s_row[PASS == 2 ? 2 * kTileM : 1];   // pass 2: (M, 1 / L) of each row
 
+    // Pass 2's blocks may take an SM as soon as one is free: they build Q before they wait for pass 1's
+    // statistics. 2 requests of the 8B shape 39 us for 45 without, 4 requests 102.5 for 101.6, the 70B shape
+    // 692-704 for 700-722; the same in pass 2, for the reduction, gains nothing.
+    if (PASS == 1) grid_dep_launch_dependents();
     const int pair = blockIdx.x / P.splits, split = blockIdx.x - pair * P.splits;
     const int h = blockIdx.y, r = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
