@@ -30,7 +30,7 @@
 // the same 8 columns; it adds those, 7 shuffles join the 8 threads of a column, and the
 // four warps meet in shared memory. Every wait is bounded, as in the prefill kernel.
 //
-// Measured (GB300): 8 requests of ~17,400 keys, 100..128 rows, 32/8 heads: 705 us, of which
+// Measured (GB300): 8 requests of ~17,400 keys, 100..128 rows, 32/8 heads: 692-709 us, of which
 // the MMAs are 430 (67 cycles each) and the rest the issuer's gaps between tiles (~500
 // cycles) and the roles' contention: without the threads' arithmetic on the scores a pass takes
 // 298 us of its 343, without the rotation 291. 16 requests of 2,112 keys, 64 rows: 103 us,
