@@ -743,3 +743,44 @@ def test_captured_and_replayed(L):
         for a, b in zip(results, want):
             assert torch.equal(a, b)
     assert s.pool.device_status() == 0
+
+
+@pytest.mark.parametrize("op", ["decode", "decode_window", "decode_mass"])
+def test_a_table_written_just_before_a_step(L, op):
+    """A kernel that rewrites the table runs directly before the step, with nothing waited for in between: the step
+    reads the new table, whichever way its own launches overlap."""
+    s = Scenario(L, [([160, 320], 10, 0), ([480], 21, 0)], seed=39)
+    R = 2
+    q, k, v = (s.dev(x) for x in step_inputs(s, R))
+    first = s.batch.entries.clone()
+    host = first.cpu().numpy().view(np.uint64).copy()
+    off = s.batch.offsets_host
+    low = np.uint64(0xFFFFFFFF)
+    for r in range(R):   # the document pages in the opposite order
+        i = np.arange(off[r], off[r] + 30)
+        host[i] = (host[i] & ~low) | (host[i[::-1]] & low)
+    second = torch.from_numpy(host.view(np.int64).copy()).cuda()
+    code = {"decode": L.LAZYATTN_OP_DECODE, "decode_mass": L.LAZYATTN_OP_DECODE_MASS}.get(op)
+    ws, n = workspace(L, s, code) if code is not None else workspace(L, s, L.LAZYATTN_OP_DECODE, 200, 4)
+    mass = torch.zeros(s.n_entries(), s.hkv, 16, device="cuda")
+
+    def step(table, wait):
+        out = s.empty(R, s.hq, s.d)
+        torch.add(table, 0, out=s.batch.entries)
+        if wait:
+            torch.cuda.synchronize()
+        if op == "decode":
+            L.lazyattn_decode(s.pool.handle, s.batch.c, q, k, v, out, ws, n)
+        elif op == "decode_window":
+            L.lazyattn_decode_window(s.pool.handle, s.batch.c, q, k, v, out, 200, 4, ws, n)
+        else:
+            L.lazyattn_decode_mass(s.pool.handle, s.batch.c, q, k, v, out, None, mass, 1.0, ws, n)
+        return out
+
+    want = [step(first, True), step(second, True)]
+    torch.cuda.synchronize()
+    assert not torch.equal(*want)
+    got = [step((first, second)[i % 2], False) for i in range(40)]
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i % 2])
+    assert s.pool.device_status() == 0
