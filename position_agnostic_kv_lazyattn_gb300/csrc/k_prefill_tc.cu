@@ -1074,19 +1074,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
-                // Rows go through this warp's 8 KB of its Q tile (whose last QK is done), 16-byte units
-                // XORed with the row, so that the stores to memory are whole rows: two a store, not a
-                // line per lane.
+                // Rows go through 8 KB of the Q tile per warp, 16-byte units XORed with the row, so that
+                // the stores to memory are whole rows: two a store, not a line per lane. Those 8 KB lie
+                // over other warps' Q rows, so they are free only once the last QK is done; without a
+                // tile nothing says that the other warps have built their rows, and zeros are stored
+                // from registers.
                 uint8_t* stage = sm + kOffQ + qi * kQBytes + quarter * 32 * 256;
+                const bool any = k >= 1 && ok;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 4 && any; ++c) {
                     uint32_t v[32];
-                    if (k >= 1 && ok) {
-                        tmem_ld32(to + 32 * c, v);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
-                    }
+                    tmem_ld32(to + 32 * c, v);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float* f = reinterpret_cast<const float*>(v + 8 * i);
@@ -1099,10 +1097,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 2
                 for (int i = 0; i < 16; ++i) {
                     const int rr = 2 * i + (lane >> 4), crow = qi * kTileM + 32 * quarter + rr, tl_ = crow >> lg;
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (any) w = *reinterpret_cast<const uint4*>(stage + rr * 256 + (((lane & 15) ^ (rr & 7)) << 4));
                     if (tl_ < ntok)
                         reinterpret_cast<uint4*>(P.out + ((size_t)(q0 + i0 + tl_) * Hq + (size_t)h * g + crow - tl_ * g) *
-                                                             kD)[lane & 15] =
-                            *reinterpret_cast<const uint4*>(stage + rr * 256 + (((lane & 15) ^ (rr & 7)) << 4));
+                                                             kD)[lane & 15] = w;
                 }
             }
         }

@@ -103,6 +103,34 @@ def test_prefill_window_rows_that_see_nothing(L):
     check_out(got, want, "bf16")
 
 
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 2), (8, 1)])
+@pytest.mark.parametrize("table", ["none", "empty entries", "before the window"])
+def test_prefill_window_without_a_live_tile(L, hq, hkv, table):
+    """No row of a request sees a key: no entries at all, entries without tokens, every token before the window (and past
+    it: the sinks). Zeros in every row, whatever q holds, beside a request that does see keys."""
+    s = Scenario(L, [([300], 10, 10)], hq=hq, hkv=hkv, seed=41)
+    words = {"none": [], "empty entries": [L.pack_entries([0], [0], [0], [0])[0]] * 9,
+             "before the window": list(s.batch.entries_host)}[table]
+    n = 300                                                    # rows of the request that sees nothing, at 1000 and on
+    ent = torch.from_numpy(np.array(words + list(s.batch.entries_host), np.uint64).view(np.int64).copy()).cuda()
+    off = torch.tensor([0, len(words), len(words) + s.n_entries()], dtype=torch.int32, device="cuda")
+    q_off = torch.tensor([0, n, n + 10], dtype=torch.int32, device="cuda")
+    big = L.DevicePool(s.pool.num_pages, hq, hkv, 128, "bf16", 1.0e4, 1400)   # the same pages, a longer position table
+    big.k_pool.copy_(s.pool.k_pool)
+    big.v_pool.copy_(s.pool.v_pool)
+    q_start = torch.tensor([1000, s.starts[0]], dtype=torch.int32, device="cuda")
+    c = L.lazyattn.make_batch(2, max(len(words), s.n_entries()), ent, off, q_off, q_start, n, n + 10)
+    q = np.concatenate([s.normal(n, hq, 128) * 2, s.q])
+    want = attend(s.spec, s.q, s.k[0], s.v[0], s.starts[0] + np.arange(10), s.pos[0], 200, 0)
+    for _ in range(20):
+        out = s.empty(n + 10, hq, 128)
+        L.lazyattn_prefill_window(big.handle, c, s.dev(q), out, 200, 0)
+        got = out.float().cpu().numpy()
+        assert np.all(got[:n] == 0)
+        check_out(got[n:], want, "bf16")
+    assert big.device_status() == 0
+
+
 @pytest.mark.parametrize("mode", ["rope", "alibi"])
 @pytest.mark.parametrize("start", [-3, 485])
 def test_rows_out_of_range(L, mode, start):
