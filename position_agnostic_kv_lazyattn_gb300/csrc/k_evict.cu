@@ -469,7 +469,9 @@ int launch_evict(const lazyattn_pool& p, const lazyattn_batch& b, const float* m
     if (cudaLaunchKernelEx(&cfg, evict_kernel, p.view(), P) != cudaSuccess) return LAZYATTN_ECUDA;
     const bool wide = p.d.head_dim * (p.d.dtype == LAZYATTN_F32 ? 4 : 2) == 512;   // 16-byte vectors a row: 32, else 16
     const int rows = kCopyThreads / (wide ? 32 : 16);
-    const int64_t most = std::min<int64_t>(budget, (int64_t)b.max_entries * kPage);   // a request keeps no more
+    // A request keeps no more tokens than this, in whole pages: the blocks also write the empty slots behind the
+    // last token, and a block of 512-byte rows is half a page.
+    const int64_t most = (std::min<int64_t>(budget, (int64_t)b.max_entries * kPage) + kPage - 1) / kPage * kPage;
     if (most == 0) return LAZYATTN_OK;
     if (launch_dependent(wide ? evict_copy_kernel<32> : evict_copy_kernel<16>,
                          dim3((unsigned)((most + rows - 1) / rows), p.d.n_kv_heads, b.num_requests),

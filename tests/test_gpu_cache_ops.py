@@ -471,6 +471,44 @@ def test_evict_pools(L, dtype, hq, hkv, d, mode):
     check_evict(L, s, weights_of(s, "normal", np.random.default_rng(26)), 61, 4, 10, dst_mass=False)
 
 
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("f32", 128), ("bf16", 128)])
+@pytest.mark.parametrize("budget", [5, 16, 50, 56, 57, 63])
+def test_evict_budgets_that_end_inside_a_page(L, dtype, d, budget):
+    """The rest of the last page: zeros, and no mass, for every size of a row."""
+    s = Scenario(L, [([70, 33], 40, 0), ([5, 100, 130], 17, 0), ([], 3, 0)], dtype=dtype, hq=4, hkv=2, d=d, seed=42, extra=40)
+    check_evict(L, s, weights_of(s, "normal", np.random.default_rng(43)), budget, 2, 3)
+
+
+def test_a_cut_cache_of_wide_rows_goes_on_observing(L):
+    """fp32, 512-byte rows, a budget that ends inside a page: the step after appends into that page, and its tokens' mass
+    starts from 0."""
+    s = Scenario(L, [([70, 33], 40, 0), ([5, 100, 130], 17, 0)], dtype="f32", hq=4, hkv=2, d=128, seed=46, extra=20)
+    w = [np.abs(x) for x in weights_of(s, "normal", np.random.default_rng(47))]
+    budget = 50
+    at = torch.tensor(s.pool.alloc_pages(10), device="cuda")      # what the new pages held before
+    s.pool.k_pool[at] = s.pool.v_pool[at] = float("nan")
+    s.pool.free_pages(at.tolist())
+    junk = torch.full((10, s.hkv, 16), float("nan"), device="cuda")   # and the block that new_mass may be given
+    del junk
+    mass = torch.from_numpy(s.mass_of(w).astype(np.float32)).cuda()
+    batch, kept, mass = s.batch.evict(s.pool, mass, budget, sinks=2, recent=3)
+    n = L.lazyattn_workspace_size(s.pool.handle, L.LAZYATTN_OP_DECODE_MASS, batch.c)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    q, kn, vn = step_inputs(s, 2)
+    out = s.empty(2, s.hq, s.d)
+    L.lazyattn_decode_mass(s.pool.handle, batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, mass, mass, 1.0, ws, n)
+    got = mass.cpu().numpy().reshape(2, 5, s.hkv, 16).transpose(0, 2, 1, 3).reshape(2, s.hkv, 80)
+    for r in range(2):
+        for h in range(s.hkv):
+            ids = kept_tokens(w[r][:, h], budget, 2, 3)
+            k, v = np.r_[s.k[r][ids, h], kn[r, h][None]], np.r_[s.v[r][ids, h], vn[r, h][None]]
+            ref = attend(s.spec, q[r, 2 * h:2 * h + 2][None], k[:, None], v[:, None], [budget], np.arange(budget + 1))
+            check_out(out[r, 2 * h:2 * h + 2].cpu().numpy(), ref, "f32", row=0)
+            check_mass(got[r, h, :budget + 1], np.r_[w[r][ids, h], 0.0] + ref.mass[:, 0], ref.reach)
+            assert np.all(got[r, h, budget + 1:] == 0)
+    assert s.pool.device_status() == 0
+
+
 @pytest.mark.parametrize("n_docs,budget", [(9, 700), (40, 3000), (150, 40)])
 def test_evict_long(L, n_docs, budget):
     s = Scenario(L, [([1000 - 7 * (j % 5) for j in range(n_docs)], 20, 0), ([30], 5, 0)], hq=2, hkv=2, seed=27, extra=2 * 200)
