@@ -153,14 +153,16 @@ __device__ int find_append_entry(const uint64_t* entries, int e0, int e1, int la
 }
 
 // Append k_new/v_new of request r into its tail page (called by a whole block).
-// Returns the entry's new value, and its index in `at` (-1: nothing appended), to every thread.
+// Returns the entry's new value, its index in `at` (-1: nothing appended) and the position written to
+// qpos in `m` (-1 likewise) to every thread. An unusable document offset (doc-local pools) leaves the entry as it
+// was, reported; the request's q still stands at `m`.
 // MODE: 0 stores k as given (position-free keys); 1 rotates it at its logical
 // position (pre-rotated pages of the materialising baseline); 2 at its
 // document-local position, logical - entry_delta (doc-local pools).
 template <typename T, int MODE>
 __device__ __forceinline__ uint64_t append_token(const PoolView& pv, uint64_t* entries, const int32_t* entry_offsets,
                                              const T* __restrict__ k_new, const T* __restrict__ v_new, int32_t* qpos,
-                                             const int32_t* entry_delta, int r, int& at) {
+                                             const int32_t* entry_delta, int r, int& at, int& m) {
     constexpr bool PREROT = MODE != 0;
     __shared__ int s_entry;
     __shared__ uint64_t s_e;
@@ -185,11 +187,13 @@ __device__ __forceinline__ uint64_t append_token(const PoolView& pv, uint64_t* e
     }
     __syncthreads();
     at = s_entry;
+    m = -1;
     if (at < 0) return 0ull;
     const uint64_t e = s_e;
     const uint32_t page = entry_page(e);
     const int slot = entry_nvalid(e);
     int pos = entry_start(e) + slot;
+    m = pos;
     if (MODE == 2) {   // rotate at the local position instead
         const int delta = entry_delta[s_entry];
         if (delta < 0 || delta > entry_start(e)) {
@@ -295,8 +299,8 @@ __global__ void decode_append_kernel(PoolView pv, uint64_t* entries, const int32
                                      const int32_t* entry_delta) {
     grid_dep_wait();
     grid_dep_launch_dependents();
-    int at;
-    append_token<T, MODE>(pv, entries, entry_offsets, k_new, v_new, qpos, entry_delta, blockIdx.x, at);
+    int at, m;
+    append_token<T, MODE>(pv, entries, entry_offsets, k_new, v_new, qpos, entry_delta, blockIdx.x, at, m);
 }
 
 // The append of a windowed step, then the request's live list: the entries with a
@@ -325,10 +329,9 @@ __global__ void __launch_bounds__(kListThreads)
         }
     };
     load(e0);
-    int appended;
+    int appended, m;   // m: as the attention masks with
     const uint64_t tail = append_token<__nv_bfloat16, MODE>(pv, entries, entry_offsets, k_new, v_new, qpos, entry_delta, r,
-                                                            appended);
-    const int m = appended < 0 ? -1 : entry_start(tail) + entry_nvalid(tail) - 1;
+                                                            appended, m);
     int done = 0;
     for (int base = e0; base < e1 && m >= 0; base += kListThreads * kListRun) {
         if (base > e0) load(base);

@@ -223,6 +223,22 @@ def test_windows_do_not_read_what_they_hide(L):
     check_decode_window(L, s, 100, 16, 1)
 
 
+@pytest.mark.parametrize("delta", [-1, 65])
+@pytest.mark.parametrize("window,sinks", [(9, 0), (9, 3), (25, 0), (1000, 0)])
+def test_decode_window_with_a_bad_document_offset(L, delta, window, sinks):
+    """The entry that the step's token would go into has an offset outside its document: reported, the entry takes no part,
+    and q stands where the token would have: windows that end right behind a page's last token leave that page out."""
+    s = Scenario(L, [([64], 8, 0)], "doc_local", seed=44)
+    s.batch.entry_delta[4] = delta
+    ws, n = workspace(L, s, L.LAZYATTN_OP_DECODE, window, sinks)
+    q, kn, vn = step_inputs(s, 1)
+    out = s.empty(1, s.hq, s.d)
+    L.lazyattn_decode_window(s.pool.handle, s.batch.c, s.dev(q), s.dev(kn), s.dev(vn), out, window, sinks, ws, n)
+    assert s.pool.device_status() == L.LAZYATTN_ERANGE
+    want = attend(s.spec, q[0][None], s.k[0][:64], s.v[0][:64], [72], np.arange(64), window, sinks)
+    check_out(out.float().cpu().numpy()[0], want, "bf16", True, 0)
+
+
 def test_decode_window_without_a_slot(L):
     """A request with no writable free slot: zeros, reported; the others are served."""
     s = Scenario(L, [([40], 16, 0), ([20], 5, 0)], spare=0, seed=8)
