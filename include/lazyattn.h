@@ -453,7 +453,11 @@ int lazyattn_decode_noalloc(lazyattn_pool_t pool, const lazyattn_batch* batch, c
  * Three operators that bound what a request reads or holds (no counterpart in
  * the paper): windowed attention, the attention weight each cached token has
  * received, and eviction by that weight. Document pages stay shared and
- * unchanged throughout.
+ * unchanged throughout. A request with more entries than the batch's max_entries is
+ * reported (LAZYATTN_ERANGE in the status word): the mass calls then take its first
+ * max_entries entries and leave the others' mass as it was, lazyattn_evict keeps
+ * nothing of it, lazyattn_decode_window takes max_entries entries of those with a
+ * visible token.
  *
  * Windowed attention: the key at logical position n is visible to the query at
  * position m iff
@@ -537,8 +541,9 @@ int lazyattn_decode_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, cons
  *   dst_mass     float32 [dst entries][n_kv_heads][16] parallel to dst_entries, or
  *                NULL: the kept tokens' mass, 0 in empty slots
  * The entries of a request that hold tokens must go up in position. A request where
- * they do not, or whose entries or new pages are out of range or too few, keeps
- * nothing (counts 0, kept -1, dst_mass 0) and LAZYATTN_ERANGE is recorded in the status word. The source pages are only read:
+ * they do not, or whose entries or new pages are out of range, too few or more than
+ * max_entries, keeps nothing (counts 0, kept -1, dst_mass 0) and LAZYATTN_ERANGE is
+ * recorded in the status word. The source pages are only read:
  * free those of the request's own afterwards. Position-free pools only, without
  * LAZYATTN_KEYS_PREROTATED (EINVAL): other layouts hold keys turned to their place. */
 int lazyattn_evict(lazyattn_pool_t pool, const lazyattn_batch* batch, const float* mass, int32_t budget, int32_t sinks,

@@ -31,6 +31,7 @@ struct Params {
     const int32_t* decode_qpos;   // decode: position of the appended token, -1 if none (else NULL)
     int32_t total_q;
     int32_t max_rows;             // prefill: rows per request that rows_kernel covers
+    int32_t cap;                  // entries per request that take part (mass: the host's bound)
     int32_t window, sinks;
     int32_t causal;               // keys past the row's position are hidden
     int32_t rotate_k;             // 0: pre-rotated pages
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     float mx = -INFINITY, l = 0.f, acc[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) acc[j] = 0.f;
-    const int e0 = P.entry_offsets[r], e1 = P.entry_offsets[r + 1];
+    const int e0 = P.entry_offsets[r], e1 = e0 + min(P.entry_offsets[r + 1] - e0, P.cap);
     int rank = 0;   // live entries before this chunk
     for (int c = e0; c < e1; c += 32) {
         const uint64_t mine = c + lane < e1 ? P.entries[c + lane] : 0ull;
@@ -213,8 +214,10 @@ __global__ void __launch_bounds__(kWarps * 32)
     mass_kernel(PoolView pv, Params P, const float* mass_in, float* mass_out, float decay) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.z, h = blockIdx.y;
-    const int i = P.entry_offsets[r] + (int)blockIdx.x * kWarps + warp;
-    if (i >= P.entry_offsets[r + 1]) return;
+    const int e0 = P.entry_offsets[r], E = P.entry_offsets[r + 1] - e0;
+    if (E > P.cap && blockIdx.x == 0 && h == 0 && threadIdx.x == 0) record_error(pv.status, LAZYATTN_ERANGE);
+    const int i = e0 + (int)blockIdx.x * kWarps + warp;
+    if (i >= e0 + min(E, P.cap)) return;
     const int g = pv.hq / pv.hkv;
     const uint64_t e = P.entries[i];
     const int n = slots_of(pv, e);
@@ -269,6 +272,7 @@ Params make_params(const lazyattn_pool& p, const lazyattn_batch& b, const int32_
     P.decode_qpos = decode_qpos;
     P.total_q = decode_qpos ? b.num_requests : b.total_q;
     P.max_rows = b.max_q_len;
+    P.cap = INT32_MAX;
     P.window = window;
     P.sinks = sinks;
     P.causal = causal;
@@ -314,6 +318,7 @@ int launch_mass_simt(const lazyattn_pool& p, const lazyattn_batch& b, const void
                      const int32_t* decode_qpos, const float* mass_in, float* mass_out, float decay, void* ws,
                      cudaStream_t stream) {
     Params P = make_params(p, b, decode_qpos, INT32_MAX, 0, decode_qpos == nullptr);
+    P.cap = b.max_entries;
     P.stats = static_cast<float2*>(ws);
     P.q_rot = reinterpret_cast<float*>(static_cast<char*>(ws) +
                                        up256((size_t)P.total_q * (size_t)p.d.n_q_heads * sizeof(float2)));

@@ -744,8 +744,9 @@ __global__ void __launch_bounds__(kMassThreads)
     const int r = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = G ? G : P.g, S = P.splits;
     grid_dep_launch_dependents();
-    const int e0 = P.entry_offsets[r], E = min(P.entry_offsets[r + 1] - e0, P.list_cap);
+    const int e0 = P.entry_offsets[r], all = P.entry_offsets[r + 1] - e0, E = min(all, P.list_cap);
     grid_dep_wait();
+    if (all > E && blockIdx.x == 0 && h == 0 && tid == 0) record_error(pv.status, LAZYATTN_ERANGE);
     const int m = P.qpos[r];
     const size_t rh = (size_t)r * pv.hkv + h;
 

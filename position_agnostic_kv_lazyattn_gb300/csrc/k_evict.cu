@@ -102,6 +102,7 @@ struct EvictParams {
     int32_t* kept;
     float* dst_mass;
     int32_t budget, sinks, recent;
+    int32_t cap;         // entries per request (host bound, by which the copy is sized)
     int32_t seg;         // entries of a share held at a time (at most kSeg)
 };
 
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(PoolView pv, EvictPa
     }
     cluster.sync();
     int n_tok = 0, base = 0, end = 0;
-    bool bad = false;
+    bool bad = E > P.cap;
     for (int c = 0; c < C; ++c) {
         const Shared* o = cluster.map_shared_rank(&S, c);
         bad = bad || o->first < end;
@@ -453,6 +454,7 @@ int launch_evict(const lazyattn_pool& p, const lazyattn_batch& b, const float* m
     P.budget = budget;
     P.sinks = sinks;
     P.recent = recent;
+    P.cap = b.max_entries;
     P.seg = std::min(kSeg, std::max(1, (b.max_entries + C - 1) / C));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C, p.d.n_kv_heads, b.num_requests);

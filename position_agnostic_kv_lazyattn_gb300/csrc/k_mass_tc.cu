@@ -778,6 +778,7 @@ __global__ void __launch_bounds__(256)
     const int e0 = P.entry_offsets[r], E = P.entry_offsets[r + 1] - e0;
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int i = (int)(at / per), rest = (int)(at - (int64_t)i * per);
+    if (at == 0 && E > P.cap) record_error(pv.status, LAZYATTN_ERANGE);
     if (i >= min(E, P.cap)) return;
     const uint64_t e = P.entries[e0 + i];
     const int n = LOCAL ? usable_local(pv, e, P.entry_delta[e0 + i]) : usable_tokens(pv, e);

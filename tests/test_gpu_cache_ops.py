@@ -648,6 +648,57 @@ def test_calls_on_a_stream_of_their_own(L):
     assert torch.equal(out, want) and torch.equal(mass, mass2) and torch.equal(kept, kept2)
 
 
+# ------------------------------------------------------------------------------------------------ a wrong bound
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("op", ["evict", "decode_mass", "prefill_mass"])
+def test_more_entries_than_the_batch_says(L, op, dtype):
+    """max_entries below a request's entries: reported; eviction keeps nothing of it, mass and output take the first
+    max_entries entries and leave the others' mass alone; the request within the bound is served."""
+    s = Scenario(L, [([100], 30, 8), ([20], 9, 4)], dtype=dtype, hq=4, hkv=2, seed=45, extra=12)
+    b, cap = s.batch, 6                                                       # the requests have 10 and 4 entries
+    b.c = L.lazyattn.make_batch(2, cap, b.entries, b.entry_offsets, b.q_offsets, b.q_start, b.max_q_len, b.total_q)
+    if op == "evict":
+        pages = s.pool.alloc_pages(12)
+        dst = torch.from_numpy(L.pack_entries(pages, [0] * 12, [0] * 12, [1] * 12).view(np.int64).copy()).cuda()
+        off = torch.tensor([0, 10, 12], dtype=torch.int32, device="cuda")
+        kept = torch.full((2, s.hkv, 125), -7, dtype=torch.int32, device="cuda")
+        mass = torch.full((s.n_entries(), s.hkv, 16), 0.5, device="cuda")
+        dm = torch.full((12, s.hkv, 16), float("nan"), device="cuda")
+        k0 = s.pool.k_pool.clone()
+        L.lazyattn_evict(s.pool.handle, b.c, mass, 125, 0, 0, dst, off, kept, dm)
+        assert s.pool.device_status() == L.LAZYATTN_ERANGE
+        assert [oracle.unpack_entry(int(e))[2] for e in dst.cpu().numpy().view(np.uint64)] == [0] * 10 + [16, 13]
+        assert bool((kept[0] == -1).all()) and bool((dm[:10] == 0).all())
+        assert torch.equal(kept[1].cpu(), torch.cat([torch.arange(29), torch.full((96,), -1)]).int().expand(s.hkv, 125))
+        touched = (s.pool.k_pool != k0).flatten(1).any(1).cpu().numpy().nonzero()[0]
+        assert set(touched) == set(pages[10:])
+        return
+    got = torch.full((s.n_entries(), s.hkv, 16), float("nan"), device="cuda")
+    take = [16 * cap, 29]                                                     # tokens of the entries that take part
+    if op == "decode_mass":
+        ws, n = workspace(L, s, L.LAZYATTN_OP_DECODE_MASS)
+        q, kn, vn = step_inputs(s, 2)
+        out = s.empty(2, s.hq, s.d)
+        L.lazyattn_decode_mass(s.pool.handle, b.c, s.dev(q), s.dev(kn), s.dev(vn), out, None, got, 1.0, ws, n)
+        ks = [s.k[0][:96], np.r_[s.k[1], kn[1][None]]]
+        vs = [s.v[0][:96], np.r_[s.v[1], vn[1][None]]]
+        refs = [attend(s.spec, q[r][None], ks[r], vs[r], [130 if r == 0 else 29], np.arange(len(ks[r]))) for r in range(2)]
+        for r in range(2):
+            check_out(out.float().cpu().numpy()[r], refs[r], dtype, row=0)
+    else:
+        ws, n = workspace(L, s, L.LAZYATTN_OP_PREFILL_MASS)
+        L.lazyattn_prefill_mass(s.pool.handle, b.c, s.dev(s.q), None, got, 1.0, ws, n)
+        refs = [attend(s.spec, s.q[s.row_slice(r)], s.k[r][:take[r]], s.v[r][:take[r]], s.starts[r] + np.arange(s.rows[r]),
+                       np.arange(take[r])) for r in range(2)]
+    assert s.pool.device_status() == L.LAZYATTN_ERANGE
+    got = got.cpu().numpy()
+    assert np.all(np.isnan(got[cap:10]))
+    got[cap:10] = 0
+    pad = [np.r_[refs[0].mass, np.zeros((34 + (op == "decode_mass"), s.hkv))], refs[1].mass]
+    check_mass(got, s.mass_of(pad), max(x.reach for x in refs))
+
+
 # ------------------------------------------------------------------------------------------------ refusals
 
 def test_refusals(L):
