@@ -1127,7 +1127,7 @@ __global__ void __launch_bounds__(256)
     const int TQ = kRows / g;
     const int q0 = P.q_offsets[r], q1 = P.q_offsets[r + 1];
     const int tok = qp * TQ + row / g, jh = row % g;
-    if (tok >= q1 - q0) return;
+    if (tok >= q1 - q0 || q1 > P.total_q) return;   // (past total_q: reported, and without partials)
     const size_t base = (size_t)item * P.splits * kRows + row;
     float M = -INFINITY;
     for (int sp = 0; sp < P.splits; ++sp) {

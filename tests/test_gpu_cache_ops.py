@@ -699,6 +699,32 @@ def test_more_entries_than_the_batch_says(L, op, dtype):
     check_mass(got, s.mass_of(pad), max(x.reach for x in refs))
 
 
+@pytest.mark.parametrize("op", ["prefill", "prefill_window"])
+def test_split_rows_past_total_q(L, op):
+    """A request whose rows end past total_q, in a call that splits the keys over several blocks: reported, and nothing is
+    written for it, neither its rows inside total_q nor what lies behind."""
+    s = Scenario(L, [([900] * 4, 20, 20), ([500], 30, 30)], seed=48)
+    b, top = s.batch, 40                                                      # rows 0..19, 20..49; total_q 40
+    c = L.lazyattn.make_batch(2, b.max_entries, b.entries, b.entry_offsets, b.q_offsets, b.q_start, b.max_q_len, top)
+    out = s.empty(64, s.hq, s.d)
+    if op == "prefill":
+        n = L.lazyattn_workspace_size(s.pool.handle, L.LAZYATTN_OP_PREFILL, c)
+    else:
+        n = L.lazyattn_window_workspace_size(s.pool.handle, L.LAZYATTN_OP_PREFILL, c, 3000, 4)
+    assert n > 256                                                            # room for partials: the call splits
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    q = s.dev(s.q)
+    if op == "prefill":
+        L.lazyattn_prefill(s.pool.handle, c, q, out, ws, n)
+    else:
+        L.lazyattn_prefill_window(s.pool.handle, c, q, out, 3000, 4, ws, n)
+    assert s.pool.device_status() == L.LAZYATTN_ERANGE
+    got = out.float().cpu().numpy()
+    assert np.all(np.isnan(got[20:]))
+    want = attend(s.spec, s.q[:20], s.k[0], s.v[0], s.starts[0] + np.arange(20), s.pos[0], 3000 if op != "prefill" else None, 4)
+    check_out(got[:20], want, "bf16")
+
+
 # ------------------------------------------------------------------------------------------------ refusals
 
 def test_refusals(L):
