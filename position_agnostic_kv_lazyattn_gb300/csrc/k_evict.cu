@@ -371,10 +371,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(PoolView pv, EvictPa
             at += P.seg;
         });
     }
-    for (int j = cnt + rank * kThreads + tid; j < P.budget; j += C * kThreads) kept[j] = -1;
+    for (int64_t j = cnt + rank * kThreads + tid; j < P.budget; j += C * kThreads) kept[j] = -1;   // budgets up to 2^31 - 1
     const int used = (cnt + kPage - 1) / kPage * kPage;
     if (P.dst_mass)
-        for (int j = used + rank * kThreads + tid; j < DE * kPage; j += C * kThreads)
+        for (int64_t j = used + rank * kThreads + tid; j < (int64_t)DE * kPage; j += C * kThreads)
             P.dst_mass[((size_t)(d0 + j / kPage) * hkv + h) * kPage + j % kPage] = 0.f;
     cluster.sync();   // no block leaves while another reads its shared memory
 }

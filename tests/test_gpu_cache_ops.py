@@ -531,6 +531,21 @@ def test_evict_long(L, n_docs, budget):
     check_evict(L, s, weights_of(s, "ties", np.random.default_rng(28)), budget, 4, 33)
 
 
+@pytest.mark.parametrize("budget", [2**31 - 1, 2**31 - 5000])
+def test_evict_with_the_largest_budgets(L, budget):
+    """`kept` of 8 GB for a short cache: everything stays, the rest of it is -1."""
+    s = Scenario(L, [([20], 9, 0)], hq=2, hkv=1, seed=49, extra=4)
+    pages = s.pool.alloc_pages(3)
+    dst = torch.from_numpy(L.pack_entries(pages, [0] * 3, [0] * 3, [1] * 3).view(np.int64).copy()).cuda()
+    off = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    kept = torch.full((1, 1, budget), -7, dtype=torch.int32, device="cuda")
+    mass = torch.rand(s.n_entries(), 1, 16, device="cuda")
+    L.lazyattn_evict(s.pool.handle, s.batch.c, mass, budget, 4, 8, dst, off, kept)
+    assert s.pool.device_status() == 0
+    assert torch.equal(kept[0, 0, :29].cpu(), torch.arange(29).int()) and bool((kept[0, 0, 29:] == -1).all())
+    assert [oracle.unpack_entry(int(e))[2] for e in dst.cpu().numpy().view(np.uint64)] == [16, 13, 0]
+
+
 def test_evict_refuses_bad_tables_on_the_device(L):
     """Entries that go down in position, a page out of range, too few new entries, a new page out of range: that request
     keeps nothing and is reported; the other request is served."""
