@@ -9,7 +9,9 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
+
+import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "liblazyattn.so")
@@ -70,6 +72,7 @@ class lazyattn_batch(ctypes.Structure):
         ("q_offsets", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("flags", ctypes.c_int32),
         ("entry_delta", ctypes.c_void_p), ("decode_plan", ctypes.c_void_p),
     ]
+    n_entries = 0   # entries of all requests, as far as make_batch was told: what a mass buffer must cover
 
 
 class lazyattn_decode_plan_stats(ctypes.Structure):
@@ -157,29 +160,69 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())   # a tenth of current_stream()'s cost
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-_DTYPE_NAMES = {}   # torch dtype -> its name, filled on use (torch is not imported here)
+class _Shape(NamedTuple):
+    """What a pool's tensors look like: elements of a query token, of a K or V token, KV heads, type, device."""
+    q: int = 0
+    kv: int = 0
+    heads: int = 0
+    dtype: object = None
+    device: Optional[int] = None
 
 
-def _dense(where: str, *tensors, dtype=None):
-    """Refuse tensors whose elements are not laid out densely (the C ABI takes plain
-    pointers) or, where dtype names are given, are of another type."""
-    for t in tensors:
-        if not hasattr(t, "is_contiguous"):   # None, or a plain address
-            continue
-        ok = t.is_contiguous()
-        if ok and dtype:
-            name = _DTYPE_NAMES.get(t.dtype)
-            if name is None:
-                name = _DTYPE_NAMES[t.dtype] = str(t.dtype).split(".")[-1]
-            ok = name in dtype
-        if not ok:
-            raise LazyAttnError(LAZYATTN_EINVAL, f"{where}: needs a contiguous tensor" +
-                                (f" of {' or '.join(dtype)}" if dtype else ""))
+_POOLS = {}         # pool handle -> _Shape, while the pool lives
+_UNKNOWN = _Shape()
+_Tensor, _F32, _I32, _I64 = torch.Tensor, torch.float32, torch.int32, torch.int64
+
+
+def _shape(desc) -> _Shape:
+    return _Shape(desc.n_q_heads * desc.head_dim, desc.n_kv_heads * desc.head_dim, desc.n_kv_heads,
+                  torch.float32 if desc.dtype == LAZYATTN_F32 else torch.bfloat16, torch.cuda.current_device())
+
+
+def _buffers(where: str, pool: _Shape, *specs):
+    """Addresses of a call's tensors; refuses those that it would misread, or read or write past
+    (the C ABI takes plain pointers). spec: (tensor, type, elements needed). A step of one request is bound
+    by its host time, so the usual case is one expression."""
+    at, device = [], pool.device
+    for t, dtype, need in specs:
+        if (t.__class__ is _Tensor and t.dtype is dtype and t.numel() >= need and t.get_device() == device and
+                t.is_contiguous()):
+            at.append(t.data_ptr())
+        else:
+            at.append(_buffer(where, pool, t, dtype, need))
+    return at
+
+
+def _buffer(where: str, pool: _Shape, t, dtype, need: int):
+    """One of _buffers: None and plain addresses pass, and so does what an unknown pool leaves open."""
+    if not hasattr(t, "data_ptr"):
+        return _ptr(t)
+    types = (_I64, torch.uint64) if dtype is _I64 else (dtype,)    # table entries: 64 bits either way
+    if (t.is_contiguous() and t.numel() >= need and (pool.device is None or t.get_device() == pool.device) and
+            (dtype is None or t.dtype in types)):
+        return t.data_ptr()
+    raise LazyAttnError(LAZYATTN_EINVAL, f"{where}: needs a contiguous tensor" +
+                        (" of " + " or ".join(str(x).split(".")[-1] for x in types) if dtype else "") +
+                        (f" with {need} elements or more" if need > 0 else "") +
+                        (f" on cuda:{pool.device}" if pool.device is not None else ""))
+
+
+def _workspace(where: str, t, nbytes: int):
+    """Address of a workspace; refuses one of fewer bytes than the call is told."""
+    if hasattr(t, "nbytes") and t.nbytes < nbytes:
+        raise LazyAttnError(LAZYATTN_EINVAL, f"{where}: the workspace has fewer than workspace_bytes bytes")
+    return _ptr(t)
+
+
+def _pool_stream(pool: _Shape, stream) -> Optional[int]:
+    """_stream for a call that the C library refuses unless the pool's device is the current one."""
+    if stream is None and pool.device is not None:
+        return torch._C._cuda_getCurrentRawStream(pool.device)
+    return _stream(stream)
 
 
 # --------------------------------------------------------------------- host helpers
@@ -202,10 +245,12 @@ def lazyattn_pool_create(desc: lazyattn_pool_desc, stream=None) -> int:
     out = ctypes.c_void_p()
     _check(lib.lazyattn_pool_create(ctypes.byref(desc), _stream(stream), ctypes.byref(out)),
            "lazyattn_pool_create")
+    _POOLS[out.value] = _shape(desc)
     return out.value
 
 
 def lazyattn_pool_destroy(pool: int):
+    _POOLS.pop(pool, None)
     _check(lib.lazyattn_pool_destroy(pool), "lazyattn_pool_destroy")
 
 
@@ -238,11 +283,14 @@ def lazyattn_store_doc(pool: int, k, v, n_tokens: int, stream=None):
 # --------------------------------------------------------------------- batches
 
 def make_batch(num_requests, max_entries, entries, entry_offsets, q_offsets=None, q_start=None,
-               max_q_len=0, total_q=0, flags=0, entry_delta=None, decode_plan=None) -> lazyattn_batch:
+               max_q_len=0, total_q=0, flags=0, entry_delta=None, decode_plan=None, n_entries=None) -> lazyattn_batch:
     """Fill a lazyattn_batch from device tensors (int64 entries, int32 offsets and deltas)
-    and a decode plan handle (or None)."""
-    return lazyattn_batch(num_requests, max_entries, max_q_len, total_q, _ptr(entries), _ptr(entry_offsets),
-                          _ptr(q_offsets), _ptr(q_start), flags, _ptr(entry_delta), decode_plan)
+    and a decode plan handle (or None). n_entries: entries of all requests, where that is not the length of the
+    entries tensor; mass buffers are checked against it."""
+    b = lazyattn_batch(num_requests, max_entries, max_q_len, total_q, _ptr(entries), _ptr(entry_offsets),
+                       _ptr(q_offsets), _ptr(q_start), flags, _ptr(entry_delta), decode_plan)
+    b.n_entries = n_entries if n_entries is not None else entries.numel() if hasattr(entries, "numel") else 0
+    return b
 
 
 # --------------------------------------------------------------------- decode plans
@@ -323,48 +371,61 @@ def lazyattn_prefill_window(pool: int, batch: lazyattn_batch, q, out, window: in
                             workspace_bytes: int = 0, stream=None):
     """lazyattn_prefill where a key at position n is visible to a row at m iff
     n <= m and (m - n < window or n < sinks)."""
-    _dense("lazyattn_prefill_window", q, out)
-    _check(lib.lazyattn_prefill_window(pool, ctypes.byref(batch), _ptr(q), _ptr(out), window, sinks, _ptr(workspace),
-                                       workspace_bytes, _stream(stream)), "lazyattn_prefill_window")
+    name, p = "lazyattn_prefill_window", _POOLS.get(pool, _UNKNOWN)
+    n = batch.total_q * p.q
+    q, out = _buffers(name, p, (q, p.dtype, n), (out, p.dtype, n))
+    _check(lib.lazyattn_prefill_window(pool, ctypes.byref(batch), q, out, window, sinks,
+                                       _workspace(name, workspace, workspace_bytes), workspace_bytes,
+                                       _pool_stream(p, stream)), name)
 
 
 def lazyattn_decode_window(pool: int, batch: lazyattn_batch, q, k_new, v_new, out, window: int, sinks: int, workspace,
                            workspace_bytes: int, stream=None):
     """lazyattn_decode under the rule of lazyattn_prefill_window."""
-    _dense("lazyattn_decode_window", q, k_new, v_new, out)
-    _check(lib.lazyattn_decode_window(pool, ctypes.byref(batch), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out), window,
-                                      sinks, _ptr(workspace), workspace_bytes, _stream(stream)), "lazyattn_decode_window")
+    name, p, R = "lazyattn_decode_window", _POOLS.get(pool, _UNKNOWN), batch.num_requests
+    n, n_new, t = R * p.q, R * p.kv, p.dtype
+    q, k_new, v_new, out = _buffers(name, p, (q, t, n), (k_new, t, n_new), (v_new, t, n_new), (out, t, n))
+    _check(lib.lazyattn_decode_window(pool, ctypes.byref(batch), q, k_new, v_new, out, window, sinks,
+                                      _workspace(name, workspace, workspace_bytes), workspace_bytes,
+                                      _pool_stream(p, stream)), name)
 
 
 def lazyattn_prefill_mass(pool: int, batch: lazyattn_batch, q, mass_in, mass_out, decay: float, workspace,
                           workspace_bytes: int, stream=None):
     """mass_out = decay * mass_in + the attention weight each cached token gets from
     the rows of q (float32 [entries][n_kv_heads][16]; mass_in None: nothing yet)."""
-    _dense("lazyattn_prefill_mass", q)
-    _dense("lazyattn_prefill_mass", mass_in, mass_out, dtype=("float32",))
-    _check(lib.lazyattn_prefill_mass(pool, ctypes.byref(batch), _ptr(q), _ptr(mass_in), _ptr(mass_out), decay,
-                                     _ptr(workspace), workspace_bytes, _stream(stream)), "lazyattn_prefill_mass")
+    name, p = "lazyattn_prefill_mass", _POOLS.get(pool, _UNKNOWN)
+    n = batch.n_entries * p.heads * PAGE_SIZE
+    q, mass_in, mass_out = _buffers(name, p, (q, p.dtype, batch.total_q * p.q), (mass_in, _F32, n), (mass_out, _F32, n))
+    _check(lib.lazyattn_prefill_mass(pool, ctypes.byref(batch), q, mass_in, mass_out, decay,
+                                     _workspace(name, workspace, workspace_bytes), workspace_bytes,
+                                     _pool_stream(p, stream)), name)
 
 
 def lazyattn_decode_mass(pool: int, batch: lazyattn_batch, q, k_new, v_new, out, mass_in, mass_out, decay: float,
                          workspace, workspace_bytes: int, stream=None):
     """lazyattn_decode and the attention weight of its step, as in lazyattn_prefill_mass."""
-    _dense("lazyattn_decode_mass", q, k_new, v_new, out)
-    _dense("lazyattn_decode_mass", mass_in, mass_out, dtype=("float32",))
-    _check(lib.lazyattn_decode_mass(pool, ctypes.byref(batch), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out),
-                                    _ptr(mass_in), _ptr(mass_out), decay, _ptr(workspace), workspace_bytes,
-                                    _stream(stream)), "lazyattn_decode_mass")
+    name, p, R = "lazyattn_decode_mass", _POOLS.get(pool, _UNKNOWN), batch.num_requests
+    n, n_new, n_mass, t = R * p.q, R * p.kv, batch.n_entries * p.heads * PAGE_SIZE, p.dtype
+    q, k_new, v_new, out, mass_in, mass_out = _buffers(name, p, (q, t, n), (k_new, t, n_new), (v_new, t, n_new),
+                                                       (out, t, n), (mass_in, _F32, n_mass), (mass_out, _F32, n_mass))
+    _check(lib.lazyattn_decode_mass(pool, ctypes.byref(batch), q, k_new, v_new, out, mass_in, mass_out, decay,
+                                    _workspace(name, workspace, workspace_bytes), workspace_bytes,
+                                    _pool_stream(p, stream)), name)
 
 
 def lazyattn_evict(pool: int, batch: lazyattn_batch, mass, budget: int, sinks: int, recent: int, dst_entries,
                    dst_offsets, kept, dst_mass=None, stream=None):
     """Copy the `budget` tokens each KV head keeps (first `sinks`, last `recent`, the
     rest by mass) into the pages of dst_entries, at positions 0, 1, ..."""
-    _dense("lazyattn_evict", mass, dst_mass, dtype=("float32",))
-    _dense("lazyattn_evict", dst_offsets, kept, dtype=("int32",))
-    _dense("lazyattn_evict", dst_entries, dtype=("int64", "uint64"))
-    _check(lib.lazyattn_evict(pool, ctypes.byref(batch), _ptr(mass), budget, sinks, recent, _ptr(dst_entries),
-                              _ptr(dst_offsets), _ptr(kept), _ptr(dst_mass), _stream(stream)), "lazyattn_evict")
+    name, p, R = "lazyattn_evict", _POOLS.get(pool, _UNKNOWN), batch.num_requests
+    slots = p.heads * PAGE_SIZE
+    n_dst = dst_entries.numel() if hasattr(dst_entries, "numel") else 0
+    mass, dst_entries, dst_offsets, kept, dst_mass = _buffers(
+        name, p, (mass, _F32, batch.n_entries * slots), (dst_entries, _I64, 0), (dst_offsets, _I32, R + 1),
+        (kept, _I32, R * p.heads * budget), (dst_mass, _F32, n_dst * slots))
+    _check(lib.lazyattn_evict(pool, ctypes.byref(batch), mass, budget, sinks, recent, dst_entries, dst_offsets, kept,
+                              dst_mass, _pool_stream(p, stream)), name)
 
 
 def lazyattn_materialize(pool: int, batch: lazyattn_batch, dst_entries, stream=None):

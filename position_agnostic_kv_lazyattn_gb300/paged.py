@@ -154,7 +154,8 @@ class Batch:
         self.flags = flags
         self.plan = None
         self.c = L.make_batch(self.num_requests, self.max_entries, self.entries, self.entry_offsets,
-                              self.q_offsets, self.q_start, self.max_q_len, self.total_q, flags, self.entry_delta)
+                              self.q_offsets, self.q_start, self.max_q_len, self.total_q, flags, self.entry_delta,
+                              n_entries=len(pg))
 
     def plan_decode(self, pool: "DevicePool", stream=None) -> dict:
         """Build the document-major decode plan of this batch's table
@@ -228,7 +229,7 @@ class Batch:
         b.entry_delta = torch.from_numpy(b.delta_host).to(device)
         b.q_offsets = b.q_start = None
         b.total_q = b.max_q_len = 0
-        b.c = L.make_batch(R, per, b.entries, b.entry_offsets, entry_delta=b.entry_delta)
+        b.c = L.make_batch(R, per, b.entries, b.entry_offsets, entry_delta=b.entry_delta, n_entries=R * per)
         return b, kept, new_mass
 
     def with_entries(self, entries_host: np.ndarray, flags: int, device="cuda") -> "Batch":
@@ -240,5 +241,5 @@ class Batch:
         b.entries = torch.from_numpy(b.entries_host.view(np.int64).copy()).to(device)
         b.flags = flags
         b.c = L.make_batch(b.num_requests, b.max_entries, b.entries, b.entry_offsets, b.q_offsets, b.q_start,
-                           b.max_q_len, b.total_q, flags, b.entry_delta)
+                           b.max_q_len, b.total_q, flags, b.entry_delta, n_entries=int(b.offsets_host[-1]))
         return b
