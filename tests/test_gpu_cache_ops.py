@@ -663,6 +663,28 @@ def test_calls_on_a_stream_of_their_own(L):
     assert torch.equal(out, want) and torch.equal(mass, mass2) and torch.equal(kept, kept2)
 
 
+# ------------------------------------------------------------------------------------------------ long tables, every layout
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("hq,hkv,window", [(8, 2, 3000), (8, 1, 2300), (2, 2, 4000)])
+def test_prefill_window_split_modes(L, mode, hq, hkv, window):
+    """Windows of so many tiles that several blocks share them, in every layout: ragged documents, rows of one block and
+    of two, a request whose window is all it has."""
+    s = Scenario(L, [([900, 77, 900, 1000, 1000], 70, 70), ([500, 1000, 1000, 33], 21, 9), ([], 60, 60)], mode, hq=hq, hkv=hkv,
+                 seed=50)
+    assert workspace(L, s, L.LAZYATTN_OP_PREFILL, window, 20)[1] > 256       # room for partials: the call splits
+    check_prefill_window(L, s, window, 20)
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_long_modes(L, mode):
+    """The other calls over tables that several blocks share, in every layout."""
+    s = Scenario(L, [([900, 77, 900, 1000], 130, 130), ([500, 1000, 33], 21, 9)], mode, hq=8, hkv=2, seed=51)
+    check_prefill_mass(L, s, 1.0, True)
+    for check in (lambda s: check_decode_window(L, s, 2000, 20, 2), lambda s: check_decode_mass(L, s, 0.5, 2)):
+        check(Scenario(L, [([900, 77, 900, 1000], 130, 0), ([500, 1000, 33], 21, 0)], mode, hq=8, hkv=2, seed=52))
+
+
 # ------------------------------------------------------------------------------------------------ a wrong bound
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
