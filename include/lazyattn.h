@@ -498,9 +498,11 @@ int lazyattn_decode_window(lazyattn_pool_t pool, const lazyattn_batch* batch, co
  * (nothing accumulated yet: decay is then unused). 0 <= decay <= 1: 1 accumulates, less fades
  * older weight (EINVAL outside, or NaN). Every slot of the requests' entries is
  * written: slots without a token get 0; what lies behind the last entry is left as
- * it was. Scores and sums are held to fp32 accuracy for bf16 pools too (rotated q
- * and k enter the products as the sum of two fp16 numbers), the order of every
- * sum is fixed: equal calls give equal bits.
+ * it was. Scores and sums are held to fp32 accuracy for bf16 pools too: a component
+ * of the rotated k, or of the rotated q times logit_scale * log2(e), enters the
+ * products as the sum of two fp16 numbers, exact to 2^-22 of itself, or to 2^-25 where
+ * it is below 1/8 (keys of 1e-4 under queries of 1e4 lose accuracy by that). The order
+ * of every sum is fixed: equal calls give equal bits.
  *
  * lazyattn_prefill_mass: the rows of q (as in lazyattn_prefill: [total_q][n_q_heads][head_dim],
  * q_offsets, q_start, keys visible up to a row's own position) observe the cache;
@@ -528,7 +530,8 @@ int lazyattn_decode_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, cons
  * n <= budget; else the first `sinks`, the last `recent` and, of the others, those
  * with the largest mass (equal ones: the earlier; NaN counts as the least), budget
  * in all. budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget (EINVAL).
- *   mass         float32 [entries][n_kv_heads][16], parallel to batch->entries
+ *   mass         float32 [entries][n_kv_heads][16], parallel to batch->entries, 16-byte
+ *                aligned like dst_mass
  *   dst_entries  device uint64, in and out: request r's new entries are
  *                [dst_offsets[r], dst_offsets[r+1]). The caller gives each a page
  *                (distinct, and none that the batch's entries name) and the writable

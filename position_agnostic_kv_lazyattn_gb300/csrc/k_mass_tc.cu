@@ -12,7 +12,8 @@
 //
 // The scores are held to fp32 accuracy: a rotated q or k in one fp16 number would
 // be off by up to 2^-11, about 3e-4 on a weight. Each goes in as hi + lo (lo: the rounding of
-// the rest), and the accumulator takes K_lo Q_hi, K_hi Q_lo, then K_hi Q_hi, small
+// the rest; lo's own steps end at 2^-24, so a component below 1/8 is exact to 2^-25 and not to 2^-22 of
+// itself), and the accumulator takes K_lo Q_hi, K_hi Q_lo, then K_hi Q_hi, small
 // ones first. That is 24 MMAs of 128 x 128 x 16 per 128 x 128 scores, and what bounds both passes.
 //
 // CTA = (request, KV head, two blocks of 128 rows = (token, head of the group) pairs, share

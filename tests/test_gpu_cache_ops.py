@@ -304,6 +304,26 @@ def test_prefill_mass_long(L):
     check_prefill_mass(L, s, 1.0, False)
 
 
+@pytest.mark.parametrize("down", [6, 10, 14])
+def test_mass_of_small_keys_under_large_queries(L, down):
+    """Keys scaled down and queries up by 2^down: the two fp16 numbers of a key component below 1/8 are exact to 2^-25, so a
+    score is off by that times the sum of its query's components (as they enter the product), beside what
+    check_mass counts."""
+    s = Scenario(L, [([260, 40], 33, 33)], seed=53, q_scale=2.0 ** (down + 1))
+    s.pool.k_pool *= 2.0 ** -down
+    s.k[0] *= 2.0 ** -down
+    ref = attend(s.spec, s.q, s.k[0], s.v[0], s.starts[0] + np.arange(33), s.pos[0])
+    # a rotation at most sqrt(2) up in the sum of a pair's components
+    reach = float(np.abs(s.q).sum(-1).max()) * np.sqrt(2.0) * 1.4427 / np.sqrt(128)
+    ws, n = workspace(L, s, L.LAZYATTN_OP_PREFILL_MASS)
+    out = torch.full((s.n_entries(), s.hkv, 16), float("nan"), device="cuda")
+    L.lazyattn_prefill_mass(s.pool.handle, s.batch.c, s.dev(s.q), None, out, 1.0, ws, n)
+    assert s.pool.device_status() == 0
+    rel = 2 * np.log(2) * (ref.reach * 72 * 2.0 ** -24 + reach * 2.0 ** -25) + 2.0 ** -19
+    got, want = out.cpu().numpy().astype(np.float64), s.mass_of([ref.mass])
+    assert np.all(np.abs(got - want) <= rel * want + 1e-30), (np.max(np.abs(got - want) / np.maximum(want, 1e-30)), rel)
+
+
 def test_prefill_mass_without_rows(L):
     """No row at all: the weights fade, nothing is added."""
     s = Scenario(L, [([70, 33], 40, 0), ([], 3, 0)], seed=16)
