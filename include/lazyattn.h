@@ -509,7 +509,13 @@ int lazyattn_decode_window(lazyattn_pool_t pool, const lazyattn_batch* batch, co
  * no output is computed. Typically the last rows of a prompt, before the cache is cut down.
  * Rows that see no key, and requests without rows, add nothing. Workspace:
  * lazyattn_workspace_size(LAZYATTN_OP_PREFILL_MASS), required; no zero-fill needed, and
- * left in any state (zero it again before a call that wants zeros gets it). */
+ * left in any state (zero it again before a call that wants zeros gets it). For bf16
+ * pools it grows with rows times entries: one float per slot of a request's max_entries
+ * entries, KV head and block of 128 rows (row = query token and head of the group), so a prompt
+ * of 8,192 tokens that observes itself with 32 / 8 heads takes 67 MB, one of 32,768
+ * tokens 1.1 GB, one of 131,072 tokens 17 GB. To bound it, observe in chunks of rows: one call
+ * per chunk, the first with the wanted decay, the others with mass_in = mass_out and decay 1
+ * (the sums then round in another order). */
 int lazyattn_prefill_mass(lazyattn_pool_t pool, const lazyattn_batch* batch, const void* q, const float* mass_in,
                           float* mass_out, float decay, void* workspace, size_t workspace_bytes, void* stream);
 

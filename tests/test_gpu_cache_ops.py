@@ -324,6 +324,28 @@ def test_mass_of_small_keys_under_large_queries(L, down):
     assert np.all(np.abs(got - want) <= rel * want + 1e-30), (np.max(np.abs(got - want) / np.maximum(want, 1e-30)), rel)
 
 
+def test_prefill_mass_in_chunks_of_rows(L):
+    """Rows observed a chunk at a time, each onto the last one's mass: what one call over all of them gives, in a
+    workspace of one chunk."""
+    s = Scenario(L, [([500, 77], 256, 256)], seed=54, hq=8, hkv=2)
+    whole = workspace(L, s, L.LAZYATTN_OP_PREFILL_MASS)
+    q = s.dev(s.q)
+    before = np.random.default_rng(55).random((len(s.pos[0]), s.hkv)).astype(np.float32)
+    old = torch.from_numpy(s.mass_of([before]).astype(np.float32)).cuda()
+    mass = torch.full_like(old, float("nan"))
+    off = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    for i in range(4):
+        start = torch.tensor([s.starts[0] + 64 * i], dtype=torch.int32, device="cuda")
+        c = L.lazyattn.make_batch(1, s.batch.max_entries, s.batch.entries, s.batch.entry_offsets, off, start, 64, 64)
+        n = L.lazyattn_workspace_size(s.pool.handle, L.LAZYATTN_OP_PREFILL_MASS, c)
+        assert 0 < n < whole[1]
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        L.lazyattn_prefill_mass(s.pool.handle, c, q[64 * i:64 * i + 64], old if i == 0 else mass, mass, 0.5 if i == 0 else 1.0, ws, n)
+    ref = attend(s.spec, s.q, s.k[0], s.v[0], s.starts[0] + np.arange(256), s.pos[0])
+    check_mass(mass.cpu().numpy(), s.mass_of([ref.mass + 0.5 * before.astype(np.float64)]), ref.reach)
+    assert s.pool.device_status() == 0
+
+
 def test_prefill_mass_without_rows(L):
     """No row at all: the weights fade, nothing is added."""
     s = Scenario(L, [([70, 33], 40, 0), ([], 3, 0)], seed=16)
