@@ -137,3 +137,40 @@ def test_host_table_check_random_tables(P):
                 want = (rc, r)
                 break
         assert L.lazyattn_check_batch_host(packed, offs, num_pages, max_position) == want
+
+
+def test_a_table_is_its_segments_entries(P):
+    """Whole tables against segment_entries of each segment: ragged, empty and reserved segments, requests without any,
+    pages as lists, ranges and arrays; what a segment refuses, a table refuses."""
+    rng = np.random.default_rng(3)
+    for trial in range(30):
+        reqs, page = [], 0
+        for _ in range(rng.integers(0, 6)):
+            segs = []
+            for _ in range(rng.integers(0, 5)):
+                n_pages = int(rng.integers(0, 7))
+                ids = range(page, page + n_pages)
+                page += n_pages
+                kind = [list, lambda x: x, np.array, lambda x: [np.int32(i) for i in x], tuple][rng.integers(0, 5)]
+                tokens = int(rng.integers(0, 16 * n_pages + 1))
+                segs.append(P.Segment(kind(ids), int(rng.integers(0, 1 << 26)), tokens, bool(rng.integers(0, 2)),
+                                      None if rng.integers(0, 2) else int(rng.integers(0, 1000))))
+            reqs.append(segs)
+        b = P.Batch(reqs, device="cpu")
+        words, delta, offsets = [], [], [0]
+        for segs in reqs:
+            for seg in segs:
+                pg, st, nv, wr = P.segment_entries(seg)
+                words += [P.L.lazyattn_pack_entry(int(a), c, d, e) for a, c, d, e in zip(pg, st, nv, wr)]
+                delta += [seg.start if seg.delta is None else seg.delta] * len(pg)
+            offsets.append(len(words))
+        assert b.entries_host.dtype == np.uint64 and b.entries_host.tolist() == words
+        assert b.offsets_host.dtype == np.int32 and b.offsets_host.tolist() == offsets
+        assert b.delta_host.dtype == np.int32 and b.delta_host.tolist() == (delta or [0])
+        assert b.max_entries == max(np.diff(offsets), default=0) and b.c.n_entries == len(words)
+        assert b.entries.view(torch.int64).tolist()[:len(words)] == b.entries_host.view(np.int64).tolist()
+    with pytest.raises(AssertionError):
+        P.Batch([[P.Segment([1], 0, 5), P.Segment([2], 16, 17)]], device="cpu")
+    for bad in (P.Segment([-1], 0, 5), P.Segment([1], -16, 5)):
+        with pytest.raises(OverflowError):
+            P.Batch([[bad]], device="cpu")
