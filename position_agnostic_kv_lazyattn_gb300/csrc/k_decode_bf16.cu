@@ -37,11 +37,12 @@
 // the splits' partials always do; mass_kernel, launched behind, merges the
 // statistics and the outputs and turns the scores into weights.
 //
-// Measured (GB300): window of 4096, 128 requests of ~9,200 tokens, 32/8 heads: 335 us a
+// Measured (GB300): window of 4096, 128 requests of ~9,200 tokens, 32/8 heads: 338 us a
 // step for 2.15 GB (6.4 TB/s, append and list included; bound by memory). Mass, 64 requests of
 // ~6,550 tokens, 64/8 heads: 343 us for 1.73 GB and 110 MB of scores written and read
 // again; the attention alone runs at 75% of the DRAM's peak, mass_kernel takes 37 us. One
-// request (window of 1024; 2,118 tokens with mass): 15 and 13 us, three dependent kernels. Every wait on a TMA is bounded; on a timeout the warp
+// request (window of 1024 over 3,940 tokens, two dependent kernels; mass over 2,118 tokens, three): 14 and 12.5 us
+// in a graph. Every wait on a TMA is bounded; on a timeout the warp
 // drains its copies and the CTA records LAZYATTN_EDEVICE.
 #include <limits.h>
 

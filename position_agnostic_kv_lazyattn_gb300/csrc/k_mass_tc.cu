@@ -31,10 +31,10 @@
 // the same 8 columns; it adds those, 7 shuffles join the 8 threads of a column, and the
 // four warps meet in shared memory. Every wait is bounded, as in the prefill kernel.
 //
-// Measured (GB300): 8 requests of ~17,400 keys, 100..128 rows, 32/8 heads: 692-709 us, of which
+// Measured (GB300): 8 requests of ~17,400 keys, 100..128 rows, 32/8 heads: 713-718 us, of which
 // the MMAs are 430 (67 cycles each) and the rest the issuer's gaps between tiles (~500
 // cycles) and the roles' contention: without the threads' arithmetic on the scores a pass takes
-// 298 us of its 343, without the rotation 291. 16 requests of 2,112 keys, 64 rows: 103 us,
+// 298 us of its 343, without the rotation 291. 16 requests of 2,112 keys, 64 rows: 106 us,
 // where the ~8 us before a CTA's first MMA count too. Not kept: N = 64 MMAs (as slow as N = 128
 // with A in tensor memory), two issuing warps (both S buffers finish together and the pipe
 // waits for the arithmetic), all eight warps on each buffer in turn (pass 2 slower by a tenth).
@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ float2 s_row[PASS == 2 ? 2 * kTileM : 1];   // pass 2: (M, 1 / L) of each row
 
     // Pass 2's blocks may take an SM as soon as one is free: they build Q before they wait for pass 1's
-    // statistics. 2 requests of the 8B shape 39 us for 45 without, 4 requests 102.5 for 101.6, the 70B shape
-    // 692-704 for 700-722; the same in pass 2, for the reduction, gains nothing.
+    // statistics. 2 requests of the 8B shape 39 us for 45 without, 16 requests 102.5 for 101.6, 8 requests of
+    // ~17,400 keys 692-704 for 700-722 (timed side by side); the same in pass 2, for the reduction, gains nothing.
     if (PASS == 1) grid_dep_launch_dependents();
     const int pair = blockIdx.x / P.splits, split = blockIdx.x - pair * P.splits;
     const int h = blockIdx.y, r = blockIdx.z;

@@ -45,9 +45,9 @@
 // round, and the producer goes from mark to mark: walking every tile's entries on
 // one thread costs about 0.1 us a tile, which for a short window over a long
 // context is most of the kernel. Pages of a live tile without a visible key are not read.
-// Measured (GB300, 32/8 heads): an 8192-token prompt under a window of 1024: 245 us (0.53 PFLOP/s:
+// Measured (GB300, 32/8 heads): an 8192-token prompt under a window of 1024: 246 us (0.53 PFLOP/s:
 // a CTA of ten tiles of 2.3 us has 13 us of start and end); 8 requests of 33..128 rows under 8192:
-// 191 us; 16 requests of 64 rows under 512: 29 us. Only the producer reads the block
+// 190 us; 16 requests of 64 rows under 512: 30 us. Only the producer reads the block
 // table. Every wait is bounded; a timeout raises an abort flag that all roles
 // honour, drains in-flight copies and MMAs, frees TMEM and records
 // LAZYATTN_EDEVICE.

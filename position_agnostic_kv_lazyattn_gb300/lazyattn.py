@@ -1,7 +1,8 @@
 """ctypes binding of liblazyattn.so (include/lazyattn.h), same names as the C ABI.
 
 Argument marshalling only: every function forwards plain pointers and sizes to
-the C library, where all the work happens. Device buffers are torch tensors
+the C library, where all the work happens (the window, mass and eviction calls also
+look at what only the tensors tell: type, device, layout and length). Device buffers are torch tensors
 (their data_ptr()), streams are torch.cuda streams (their cuda_stream handle).
 If the compiled library is missing, importing this module raises.
 """
