@@ -217,7 +217,8 @@ class Batch:
         ceil(budget / 16) + reserve fresh, writable pages per request from the pool, and
         returns (the new Batch, kept positions int32 [R][n_kv_heads][budget],
         the new batch's mass). Later decode steps append into the reserved
-        room. The old pages are still the caller's to free. Reads the new table back to the
+        room. The old pages are still the caller's to free. A request that lazyattn_evict refuses on
+        the device (pool.device_status() tells) comes back empty. Reads the new table back to the
         host, so it waits for the stream."""
         if stream is not None:
             stream = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))

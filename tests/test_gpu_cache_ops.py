@@ -705,6 +705,58 @@ def test_calls_on_a_stream_of_their_own(L):
     assert torch.equal(out, want) and torch.equal(mass, mass2) and torch.equal(kept, kept2)
 
 
+def test_two_calls_at_once(L):
+    """Two pools' calls in flight on two streams, each with a workspace of its own: the bits of the calls one by one."""
+    both = [Scenario(L, [([900, 150], 130, 130), ([33], 20, 20)], seed=56, extra=400),
+            Scenario(L, [([400] * 6, 64, 64)], seed=57, hq=8, hkv=1, extra=400)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    work = []
+    for s in both:
+        R = len(s.rows)
+        st = dict(q=s.dev(s.q), step=[s.dev(x) for x in step_inputs(s, R)], table=s.batch.entries.clone(), R=R,
+                  wsp=workspace(L, s, L.LAZYATTN_OP_PREFILL, 700, 4), wsw=workspace(L, s, L.LAZYATTN_OP_DECODE, 700, 4),
+                  wsm=workspace(L, s, L.LAZYATTN_OP_PREFILL_MASS), wsd=workspace(L, s, L.LAZYATTN_OP_DECODE_MASS),
+                  off=torch.arange(R + 1, dtype=torch.int32, device="cuda") * 20,
+                  pages=torch.from_numpy(L.pack_entries(s.pool.alloc_pages(20 * R), [0] * 20 * R, [0] * 20 * R, [1] * 20 * R)
+                                         .view(np.int64).copy()).cuda())
+        work.append(st)
+
+    def outputs(s, st):
+        rows, R = s.batch.total_q, st["R"]
+        return dict(p=s.empty(rows, s.hq, s.d), w=s.empty(R, s.hq, s.d), d=s.empty(R, s.hq, s.d), dst=st["pages"].clone(),
+                    m=torch.zeros(s.n_entries(), s.hkv, 16, device="cuda"), n=torch.zeros(s.n_entries(), s.hkv, 16, device="cuda"),
+                    kept=torch.zeros(R, s.hkv, 300, dtype=torch.int32, device="cuda"))
+
+    def calls(s, st, o):
+        h, c, (q1, k1, v1) = s.pool.handle, s.batch.c, st["step"]
+        L.lazyattn_prefill_window(h, c, st["q"], o["p"], 700, 4, *st["wsp"])
+        L.lazyattn_prefill_mass(h, c, st["q"], None, o["m"], 1.0, *st["wsm"])
+        s.batch.entries.copy_(st["table"])
+        L.lazyattn_decode_window(h, c, q1, k1, v1, o["w"], 700, 4, *st["wsw"])
+        s.batch.entries.copy_(st["table"])
+        L.lazyattn_decode_mass(h, c, q1, k1, v1, o["d"], o["m"], o["n"], 0.5, *st["wsd"])
+        L.lazyattn_evict(h, c, o["n"], 300, 4, 16, o["dst"], st["off"], o["kept"])
+
+    want = []
+    for s, st in zip(both, work):
+        o = outputs(s, st)
+        calls(s, st, o)
+        torch.cuda.synchronize()
+        want.append(o)
+    got = [[outputs(s, st) for _ in range(10)] for s, st in zip(both, work)]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for j in (0, 1):
+            with torch.cuda.stream(streams[j]):
+                calls(both[j], work[j], got[j][i])
+    torch.cuda.synchronize()
+    for j in (0, 1):
+        for o in got[j]:
+            for name, x in o.items():
+                assert torch.equal(x, want[j][name]), (j, name)
+        assert both[j].pool.device_status() == 0
+
+
 # ------------------------------------------------------------------------------------------------ long tables, every layout
 
 @pytest.mark.parametrize("mode", MODES)
