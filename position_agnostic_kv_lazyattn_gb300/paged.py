@@ -214,7 +214,8 @@ class Batch:
               reserve: int = 1, stream=None):
         """Cut every request's cache down to `budget` tokens per KV head
         (lazyattn_evict by `mass`, float32 [entries][n_kv_heads][16]): takes
-        ceil(budget / 16) + reserve fresh, writable pages per request from the pool, and
+        ceil(budget / 16) + reserve fresh, writable pages per request from the pool (a request of
+        fewer entries than that: as many as it has, + reserve), and
         returns (the new Batch, kept positions int32 [R][n_kv_heads][budget],
         the new batch's mass). Later decode steps append into the reserved
         room. The old pages are still the caller's to free. A request that lazyattn_evict refuses on
@@ -224,31 +225,33 @@ class Batch:
             stream = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
             with torch.cuda.stream(stream):
                 return self.evict(pool, mass, budget, sinks, recent, reserve)
-        R, per = self.num_requests, -(-budget // PAGE_SIZE) + reserve
+        R = self.num_requests
+        offsets = np.concatenate([[0], np.cumsum(np.minimum(-(-budget // PAGE_SIZE), np.diff(self.offsets_host)) + reserve)])
+        offsets, total = offsets.astype(np.int32), int(offsets[-1])
         device = self.entries.device
         if tuple(mass.shape[1:]) != (pool.n_kv_heads, PAGE_SIZE) or mass.shape[0] < int(self.offsets_host[-1]):
             raise ValueError("mass must be [entries][n_kv_heads][16] of this batch's table")
-        pages = pool.alloc_pages(R * per)
+        pages = pool.alloc_pages(total)
         try:
-            dst = torch.from_numpy(pack_entries(pages, [0] * len(pages), [0] * len(pages), [1] * len(pages))
+            held = pages or [0]   # (no page at all: an entry that no request owns)
+            dst = torch.from_numpy(pack_entries(held, [0] * len(held), [0] * len(held), [1] * len(held))
                                    .view(np.int64).copy()).to(device)
-            offsets = (np.arange(R + 1) * per).astype(np.int32)
             dst_offsets = torch.from_numpy(offsets).to(device)
             kept = torch.empty((R, pool.n_kv_heads, budget), dtype=torch.int32, device=device)
-            new_mass = torch.empty((R * per, pool.n_kv_heads, PAGE_SIZE), dtype=torch.float32, device=device)
+            new_mass = torch.empty((len(held), pool.n_kv_heads, PAGE_SIZE), dtype=torch.float32, device=device)
             L.lazyattn_evict(pool.handle, self.c, mass, budget, sinks, recent, dst, dst_offsets, kept, new_mass)
         except Exception:
             pool.free_pages(pages)
             raise
         b = Batch.__new__(Batch)
-        b.num_requests, b.max_entries, b.offsets_host, b.flags, b.plan = R, per, offsets, 0, None
+        b.num_requests, b.max_entries, b.offsets_host, b.flags, b.plan = R, int(np.diff(offsets).max()), offsets, 0, None
         b.entries, b.entry_offsets = dst, dst_offsets
-        b.entries_host = dst.cpu().numpy().view(np.uint64)
-        b.delta_host = np.zeros(max(1, R * per), np.int32)
+        b.entries_host = dst.cpu().numpy().view(np.uint64)[:total]
+        b.delta_host = np.zeros(max(1, total), np.int32)
         b.entry_delta = torch.from_numpy(b.delta_host).to(device)
         b.q_offsets = b.q_start = None
         b.total_q = b.max_q_len = 0
-        b.c = L.make_batch(R, per, b.entries, b.entry_offsets, entry_delta=b.entry_delta, n_entries=R * per)
+        b.c = L.make_batch(R, b.max_entries, b.entries, b.entry_offsets, entry_delta=b.entry_delta, n_entries=total)
         return b, kept, new_mass
 
     def with_entries(self, entries_host: np.ndarray, flags: int, device="cuda") -> "Batch":

@@ -588,6 +588,37 @@ def test_evict_with_the_largest_budgets(L, budget):
     assert [oracle.unpack_entry(int(e))[2] for e in dst.cpu().numpy().view(np.uint64)] == [16, 13, 0]
 
 
+@pytest.mark.parametrize("reserve", [0, 2])
+def test_batch_evict_takes_no_more_pages_than_a_request_can_fill(L, reserve):
+    """A budget past what the short requests hold, and a pool with pages for what they do hold: served, everything of them
+    kept; a request without entries gets its reserve alone."""
+    s = Scenario(L, [([400, 300], 30, 0), ([20], 9, 0), ([], 5, 0), ([], 0, 0)], seed=58, spare=0)
+    w = [np.abs(x) for x in weights_of(s, "normal", np.random.default_rng(59))]
+    mass = torch.from_numpy(s.mass_of(w).astype(np.float32)).cuda()
+    n = [13 + reserve, 3 + reserve, 1 + reserve, reserve]                     # budget 200; 3, 1 and no entries
+    s.pool.alloc_pages(s.pool.free_count() - sum(n))
+    batch, kept, new = s.batch.evict(s.pool, mass, 200, sinks=4, recent=16, reserve=reserve)
+    assert s.pool.free_count() == 0 and s.pool.device_status() == 0
+    assert np.diff(batch.offsets_host).tolist() == n and batch.max_entries == n[0] and batch.c.n_entries == sum(n)
+    got = [oracle.unpack_entry(int(e))[2] for e in batch.entries_host]
+    assert got[:13] == [16] * 12 + [8] and got[n[0]:n[0] + 3] == [16, 13, 0] and got[n[0] + n[1]] == 5
+    new, kept = new.cpu().numpy(), kept.cpu().numpy()
+    for r in range(4):
+        for h in range(s.hkv):
+            ids = kept_tokens(w[r][:, h], 200, 4, 16) if len(w[r]) else []
+            np.testing.assert_array_equal(kept[r, h], np.r_[s.pos[r][ids] if len(ids) else [], np.full(200 - len(ids), -1)])
+            flat = new[batch.offsets_host[r]:batch.offsets_host[r + 1], h].reshape(-1)
+            np.testing.assert_array_equal(flat, np.r_[w[r][ids, h] if len(ids) else [], np.zeros(len(flat) - len(ids))])
+
+
+def test_batch_evict_of_nothing(L):
+    s = Scenario(L, [([], 0, 0), ([], 0, 0)], seed=60, spare=0)
+    mass = torch.zeros(1, s.hkv, 16, device="cuda")
+    batch, kept, new = s.batch.evict(s.pool, mass, 32, reserve=0)
+    assert s.pool.device_status() == 0 and bool((kept == -1).all())
+    assert len(batch.entries_host) == 0 and batch.max_entries == 0 and batch.c.n_entries == 0
+
+
 def test_evict_refuses_bad_tables_on_the_device(L):
     """Entries that go down in position, a page out of range, too few new entries, a new page out of range: that request
     keeps nothing and is reported; the other request is served."""
